@@ -12,6 +12,7 @@ import ctypes
 import math
 import os
 import threading
+from typing import NamedTuple
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "lib", "libfa.so")
@@ -26,8 +27,10 @@ STATUS = {
 FA_MASK_NONE, FA_MASK_BOOL, FA_MASK_F16, FA_MASK_F32 = 0, 1, 2, 3
 EXPORTS = ("fa_bwd", "fa_bwd_ex", "fa_bwd_workspace_bytes", "fa_fwd", "fa_fwd_ex", "fa_fwd_fp8",
            "fa_fwd_fp8_ex", "fa_fwd_fp8_splitkv",
-           "fa_fwd_host", "fa_fwd_host_workspace_bytes", "fa_fwd_splitkv",
-           "fa_fwd_splitkv_static", "fa_get_device_status", "fa_selftest_wait_timeout",
+           "fa_fwd_host", "fa_fwd_host_workspace_bytes", "fa_fwd_paged", "fa_fwd_splitkv",
+           "fa_fwd_splitkv_static", "fa_get_device_status", "fa_paged_plan",
+           "fa_paged_workspace_bytes", "fa_qk_norm_rope", "fa_qk_norm_rope_bwd",
+           "fa_qk_norm_rope_bwd_workspace_bytes", "fa_selftest_wait_timeout",
            "fa_splitkv_auto_splits", "fa_splitkv_workspace_bytes", "fa_status_string",
            "fa_version")
 # size of the library's static split-KV scratch (FA_STATIC_SCRATCH_BYTES)
@@ -44,6 +47,26 @@ class FaError(RuntimeError):
         self.status = status
         super().__init__(f"{where}: {STATUS.get(status, status)} "
                          f"({status_string(status) if _lib is not None else ''})")
+
+
+class FaRows(ctypes.Structure):
+    """fa_rows of include/fa.h."""
+    _fields_ = [("ptr", ctypes.c_void_p), ("stride_b", ctypes.c_longlong),
+                ("stride_l", ctypes.c_longlong), ("stride_h", ctypes.c_longlong)]
+
+
+class FaRopeArgs(ctypes.Structure):
+    """fa_rope_args of include/fa.h."""
+    _fields_ = [(n, FaRows) for n in ("q", "k", "v", "q_out", "k_out")] + \
+        [(n, ctypes.c_void_p) for n in ("q_weight", "k_weight", "cos_sin", "positions")] + \
+        [(n, ctypes.c_longlong) for n in ("positions_stride_b", "positions_stride_l")] + \
+        [(n, ctypes.c_void_p) for n in ("k_cache", "v_cache")] + \
+        [(n, ctypes.c_longlong) for n in ("cache_stride_page", "cache_stride_token",
+                                          "cache_stride_head")] + \
+        [("slots", ctypes.c_void_p)] + \
+        [(n, ctypes.c_int) for n in ("num_pages", "page_size", "positions_64", "B", "L", "H",
+                                     "H_kv", "D", "rot_dim", "max_pos", "interleaved",
+                                     "dtype")] + [("eps", ctypes.c_float)]
 
 
 def load(path: str = LIB_PATH) -> ctypes.CDLL:
@@ -94,6 +117,20 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.fa_bwd_ex.restype = i
         lib.fa_bwd_workspace_bytes.argtypes = [i, i, i, i]
         lib.fa_bwd_workspace_bytes.restype = ctypes.c_size_t
+        sz, pa = ctypes.c_size_t, ctypes.POINTER(FaRopeArgs)
+        lib.fa_paged_plan.argtypes = [vp, vp, vp, ll, vp, i, i, i, i, i, vp, vp, vp, vp, vp, vp]
+        lib.fa_paged_plan.restype = i
+        lib.fa_qk_norm_rope.argtypes = [pa, vp]
+        lib.fa_qk_norm_rope.restype = i
+        lib.fa_qk_norm_rope_bwd.argtypes = [pa, FaRows, FaRows, vp, vp, vp, sz, vp]
+        lib.fa_qk_norm_rope_bwd.restype = i
+        lib.fa_qk_norm_rope_bwd_workspace_bytes.argtypes = [i]
+        lib.fa_qk_norm_rope_bwd_workspace_bytes.restype = sz
+        lib.fa_paged_workspace_bytes.argtypes = [i]
+        lib.fa_paged_workspace_bytes.restype = sz
+        lib.fa_fwd_paged.argtypes = [vp, ll, ll, vp, vp, ll, ll, ll, vp, ll, vp, vp, vp, ll, ll, vp,
+                                     i, i, i, i, i, i, i, i, f, i, i, i, i, vp, sz, vp]
+        lib.fa_fwd_paged.restype = i
         lib.fa_splitkv_workspace_bytes.argtypes = [i, i, i, i, i]
         lib.fa_splitkv_workspace_bytes.restype = ctypes.c_size_t
         lib.fa_splitkv_auto_splits.argtypes = [i, i, i, i, i, i, i]
@@ -254,6 +291,48 @@ def choose_splits(B, H, L_q, L_k, sm_count=None, H_kv=None, D=128, dtype=FA_F16)
     used, the device's count is).  dtype 2 = E4M3 inputs."""
     return int(load().fa_splitkv_auto_splits(B, H, H if H_kv is None else H_kv, L_q, L_k, D,
                                              dtype))
+
+
+def fa_paged_plan(q_lens, ctx_lens, block_table, table_stride, free_pages, n_free, B, max_pages,
+                  page_size, num_tokens, cu_q, kv_lens, positions, slots, counts, stream) -> int:
+    """The page-table C entry point, unchanged."""
+    return load().fa_paged_plan(q_lens, ctx_lens, block_table, table_stride, free_pages, n_free, B,
+                                max_pages, page_size, num_tokens, cu_q, kv_lens, positions, slots,
+                                counts, stream)
+
+
+def fa_qk_norm_rope(args: FaRopeArgs, stream) -> int:
+    """The norm-and-rotation C entry point, unchanged."""
+    return load().fa_qk_norm_rope(ctypes.byref(args), stream)
+
+
+def fa_qk_norm_rope_bwd(args: FaRopeArgs, dq: FaRows, dk: FaRows, dq_weight, dk_weight, workspace,
+                        workspace_bytes, stream) -> int:
+    """The norm-and-rotation gradient C entry point, unchanged."""
+    return load().fa_qk_norm_rope_bwd(ctypes.byref(args), dq, dk, dq_weight, dk_weight, workspace,
+                                      int(workspace_bytes), stream)
+
+
+def fa_qk_norm_rope_bwd_workspace_bytes(D) -> int:
+    return int(load().fa_qk_norm_rope_bwd_workspace_bytes(D))
+
+
+def fa_paged_workspace_bytes(D) -> int:
+    return int(load().fa_paged_workspace_bytes(D))
+
+
+def fa_fwd_paged(q, q_stride_t, q_stride_h, k_cache, v_cache, cache_stride_page,
+                 cache_stride_token, cache_stride_head, block_table, table_stride, cu_q, kv_lens,
+                 out, out_stride_t, out_stride_h, lse, total_q, B, H, H_kv, D, num_pages,
+                 page_size, max_pages, scale, causal, window_left, window_right, dtype, workspace,
+                 workspace_bytes, stream) -> int:
+    """The paged-cache attention C entry point, unchanged."""
+    return load().fa_fwd_paged(q, q_stride_t, q_stride_h, k_cache, v_cache, cache_stride_page,
+                               cache_stride_token, cache_stride_head, block_table, table_stride,
+                               cu_q, kv_lens, out, out_stride_t, out_stride_h, lse, total_q, B, H,
+                               H_kv, D, num_pages, page_size, max_pages, float(scale),
+                               int(causal), int(window_left), int(window_right), int(dtype),
+                               workspace, int(workspace_bytes), stream)
 
 
 def fa_get_device_status(stream=None) -> int:
@@ -569,4 +648,317 @@ def flash_fwd_host(q, k, v, scale=None, causal=False, window_left=-1, window_rig
                          stream.cuda_stream)
     if st != FA_OK:
         raise FaError(st, "fa_fwd_host")
+    return out, lse
+
+
+# ------------------------------------------------------------ serving
+class PagedPlan(NamedTuple):
+    """What paged_plan returns: device tensors of one serving step."""
+    cu_q: "object"        # int32 [B + 1]
+    kv_lens: "object"     # int32 [B]
+    positions: "object"   # int32 [num_tokens]
+    slots: "object"       # int64 [num_tokens]
+    counts: "object"      # int32 [3]: new tokens, pages taken, tokens without a slot
+
+
+class _on:
+    """The given device made current, if it is not already."""
+
+    def __init__(self, index):
+        self.index, self.back = index, None
+
+    def __enter__(self):
+        import torch
+        now = torch.cuda.current_device()
+        if now != self.index:
+            torch.cuda.set_device(self.index)
+            self.back = now
+
+    def __exit__(self, *exc):
+        import torch
+        if self.back is not None:
+            torch.cuda.set_device(self.back)
+
+
+def _same_device(index, **tensors):
+    for name, t in tensors.items():
+        if t is not None and (not t.is_cuda or t.device.index != index):
+            raise ValueError(f"{name} must be a CUDA tensor on the same device")
+
+
+def _vector(name, t, dtype, n):
+    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} vector of {n}")
+
+
+def _16bit(q):
+    import torch
+    if q.dtype == torch.float16:
+        return FA_F16
+    if q.dtype == torch.bfloat16:
+        return FA_BF16
+    raise TypeError("dtype must be float16 or bfloat16")
+
+
+def _cache_layout(k_cache, v_cache, H_kv, D, dtype):
+    """(pages, page size, element strides) of caches [pages, page_size, H_kv, D]."""
+    if k_cache.dim() != 4 or tuple(k_cache.shape) != tuple(v_cache.shape) \
+            or k_cache.shape[2] != H_kv or k_cache.shape[3] != D:
+        raise ValueError("k_cache, v_cache must be [pages, page_size, H_kv, D]")
+    if k_cache.dtype != dtype or v_cache.dtype != dtype:
+        raise TypeError("k_cache, v_cache must have q's dtype")
+    st = k_cache.stride()
+    if st != v_cache.stride() or st[3] != 1:
+        raise ValueError("k_cache, v_cache must have the same strides, contiguous along D")
+    return k_cache.shape[0], k_cache.shape[1], st[0], st[1], st[2]
+
+
+def paged_plan(q_lens, ctx_lens, block_table, free_pages, page_size, num_tokens, out=None,
+               stream=None):
+    """One serving step's page tables, built on the GPU (fa_paged_plan).
+
+    q_lens, ctx_lens: int32 [B], the requests' new tokens and their tokens in
+    the cache; block_table: int32 [B, max_pages] (rows may be strided), grown
+    in place from free_pages (int32, taken from index 0); num_tokens: the
+    capacity of positions and slots (at least the new tokens; the rest, a
+    captured graph's padding, gets -1).  ``out``: a PagedPlan to write into.
+    Nothing is read back: counts[2] > 0 tells that pages ran out."""
+    import torch
+
+    B = q_lens.shape[0]
+    i32 = torch.int32
+    _vector("q_lens", q_lens, i32, B)
+    _vector("ctx_lens", ctx_lens, i32, B)
+    if block_table.dim() != 2 or block_table.dtype != i32 or block_table.shape[0] != B \
+            or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError("block_table must be int32 [B, max_pages], contiguous along the pages")
+    _vector("free_pages", free_pages, i32, free_pages.numel())
+    dev = q_lens.device.index
+    _same_device(dev, q_lens=q_lens, ctx_lens=ctx_lens, block_table=block_table,
+                 free_pages=free_pages)
+    num_tokens = int(num_tokens)
+    if out is None:
+        if num_tokens < 0:
+            raise ValueError("num_tokens must be >= 0")
+        d = q_lens.device
+        out = PagedPlan(torch.empty(B + 1, dtype=i32, device=d), torch.empty(B, dtype=i32, device=d),
+                        torch.empty(num_tokens, dtype=i32, device=d),
+                        torch.empty(num_tokens, dtype=torch.int64, device=d),
+                        torch.empty(3, dtype=i32, device=d))
+    else:
+        for name, dt, n in (("cu_q", i32, B + 1), ("kv_lens", i32, B), ("positions", i32, num_tokens),
+                            ("slots", torch.int64, num_tokens), ("counts", i32, 3)):
+            _vector(name, getattr(out, name), dt, n)
+        _same_device(dev, **out._asdict())
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    max_pages = block_table.shape[1]
+    with _on(dev):
+        st = fa_paged_plan(q_lens.data_ptr(), ctx_lens.data_ptr(), block_table.data_ptr(),
+                           block_table.stride(0) if B > 1 else max(max_pages, 1),
+                           free_pages.data_ptr(), free_pages.shape[0], B, max_pages,
+                           int(page_size), num_tokens, out.cu_q.data_ptr(),
+                           out.kv_lens.data_ptr(), out.positions.data_ptr(),
+                           out.slots.data_ptr(), out.counts.data_ptr(), stream.cuda_stream)
+    if st != FA_OK:
+        raise FaError(st, "fa_paged_plan")
+    return out
+
+
+def _rows(name, t, shape, dtype):
+    """fa_rows of a [T, H, D] or [B, L, H, D] tensor of the given shape."""
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.stride(-1) != 1:
+        raise ValueError(f"{name} must be {tuple(shape)}, {dtype}, contiguous along D")
+    s = t.stride()
+    return FaRows(t.data_ptr(), s[0] if len(s) == 4 else 0, s[-3], s[-2])
+
+
+def _rope_args(q, k, q_weight, k_weight, cos_sin, positions, eps, interleaved):
+    import torch
+
+    if q.dim() not in (3, 4) or k.dim() != q.dim() or k.shape[:-2] != q.shape[:-2] \
+            or k.shape[-1] != q.shape[-1]:
+        raise ValueError("q, k must be [T, H, D] and [T, H_kv, D], or [B, L, H, D] and "
+                         "[B, L, H_kv, D]")
+    a = FaRopeArgs()
+    a.dtype = _16bit(q)
+    a.B = q.shape[0] if q.dim() == 4 else 1
+    a.L, a.H, a.D = q.shape[-3:]
+    a.H_kv = k.shape[-2]
+    a.q = _rows("q", q, q.shape, q.dtype)
+    a.k = _rows("k", k, k.shape, q.dtype)
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _vector(name, w, q.dtype, a.D)
+            setattr(a, name, w.data_ptr())
+    if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32 or not cos_sin.is_contiguous():
+        raise ValueError("cos_sin must be a contiguous float32 [max_pos, rot_dim]")
+    a.max_pos, a.rot_dim = cos_sin.shape
+    a.cos_sin = cos_sin.data_ptr()
+    if positions.shape != q.shape[:-2] or positions.dtype not in (torch.int32, torch.int64):
+        raise ValueError("positions must be int32 or int64 of q's token axes")
+    a.positions = positions.data_ptr()
+    a.positions_64 = int(positions.dtype == torch.int64)
+    ps = positions.stride()
+    a.positions_stride_b, a.positions_stride_l = (ps[0] if len(ps) == 2 else 0), ps[-1]
+    a.eps = eps
+    a.interleaved = int(interleaved)
+    return a
+
+
+def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps=1e-6, interleaved=False,
+                 q_out=None, k_out=None, v=None, k_cache=None, v_cache=None, slots=None,
+                 stream=None):
+    """RMS norm of every query and key head and the rotary rotation, in one
+    pass (fa_qk_norm_rope); with a cache, k and v are written to it too.
+
+    q: [T, H, D] or [B, L, H, D]; k: the same with H_kv heads; fp16 or bf16,
+    contiguous along D, other strides free (views of one projection).
+    q_weight, k_weight: [D] of q's dtype, or None (no norm).  cos_sin: float32
+    [max_pos, rot_dim], the cosines then the sines.  positions: int32 or int64
+    of q's token axes; a negative one (or >= max_pos) marks padding, of which
+    nothing is written.  ``interleaved``: pairs (2i, 2i + 1) instead of
+    (i, i + rot_dim / 2).
+
+    q_out, k_out: like q, k, any strides (a [B, H, L, D] tensor transposed),
+    q and k themselves to work in place; allocated contiguous if None.  With
+    k_cache, v_cache [pages, page_size, H_kv, D] (strides free), v and slots
+    (int64, one per token; negative: not written) k_out is only written if
+    given.  Returns (q_out, k_out)."""
+    import torch
+
+    a = _rope_args(q, k, q_weight, k_weight, cos_sin, positions, eps, interleaved)
+    dev = q.device.index
+    cached = k_cache is not None or v_cache is not None
+    if cached:
+        if k_cache is None or v_cache is None or v is None or slots is None:
+            raise ValueError("a cache needs k_cache, v_cache, v and slots")
+        a.num_pages, a.page_size, a.cache_stride_page, a.cache_stride_token, \
+            a.cache_stride_head = _cache_layout(k_cache, v_cache, a.H_kv, a.D, q.dtype)
+        a.k_cache, a.v_cache = k_cache.data_ptr(), v_cache.data_ptr()
+        a.v = _rows("v", v, k.shape, q.dtype)
+        if slots.dtype != torch.int64 or slots.numel() != a.B * a.L or not slots.is_contiguous():
+            raise ValueError("slots must be contiguous int64, one per token")
+        a.slots = slots.data_ptr()
+    _same_device(dev, q=q, k=k, q_weight=q_weight, k_weight=k_weight, cos_sin=cos_sin,
+                 positions=positions, q_out=q_out, k_out=k_out, v=v, k_cache=k_cache,
+                 v_cache=v_cache, slots=slots)
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    a.q_out = _rows("q_out", q_out, q.shape, q.dtype)
+    if k_out is None and not cached:
+        k_out = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+    if k_out is not None:
+        a.k_out = _rows("k_out", k_out, k.shape, q.dtype)
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    with _on(dev):
+        st = fa_qk_norm_rope(a, stream.cuda_stream)
+    if st != FA_OK:
+        raise FaError(st, "fa_qk_norm_rope")
+    return q_out, k_out
+
+
+def qk_norm_rope_bwd(q, k, q_weight, k_weight, cos_sin, positions, dq_out, dk_out, eps=1e-6,
+                     interleaved=False, dq=None, dk=None, workspace=None, stream=None):
+    """The gradients of qk_norm_rope (fa_qk_norm_rope_bwd) from its inputs and
+    the gradients of its outputs: (dq, dk, dq_weight, dk_weight), the last two
+    float32 (None without a weight).  dq, dk: like q, k, any strides, allocated
+    contiguous if None; dq may be dq_out itself.  The workspace is allocated
+    here unless given (a uint8 CUDA tensor, 256-byte aligned)."""
+    import torch
+
+    a = _rope_args(q, k, q_weight, k_weight, cos_sin, positions, eps, interleaved)
+    dev = q.device.index
+    a.q_out = _rows("dq_out", dq_out, q.shape, q.dtype)
+    a.k_out = _rows("dk_out", dk_out, k.shape, q.dtype)
+    _same_device(dev, q=q, k=k, q_weight=q_weight, k_weight=k_weight, cos_sin=cos_sin,
+                 positions=positions, dq_out=dq_out, dk_out=dk_out, dq=dq, dk=dk,
+                 workspace=workspace)
+    if dq is None:
+        dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if dk is None:
+        dk = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+    rq, rk = _rows("dq", dq, q.shape, q.dtype), _rows("dk", dk, k.shape, q.dtype)
+    dwq = dwk = None
+    if q_weight is not None:
+        dwq = torch.empty(a.D, dtype=torch.float32, device=q.device)
+    if k_weight is not None:
+        dwk = torch.empty(a.D, dtype=torch.float32, device=q.device)
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    with _on(dev):
+        if workspace is None:
+            workspace = torch.empty(max(fa_qk_norm_rope_bwd_workspace_bytes(a.D), 1),
+                                    dtype=torch.uint8, device=q.device)
+        st = fa_qk_norm_rope_bwd(a, rq, rk, dwq.data_ptr() if dwq is not None else None,
+                                 dwk.data_ptr() if dwk is not None else None,
+                                 workspace.data_ptr(), workspace.numel(), stream.cuda_stream)
+    if st != FA_OK:
+        raise FaError(st, "fa_qk_norm_rope_bwd")
+    return dq, dk, dwq, dwk
+
+
+def flash_fwd_paged(q, k_cache, v_cache, block_table, cu_q, kv_lens, scale=None, causal=True,
+                    window_left=-1, window_right=-1, return_lse=True, out=None, lse=None,
+                    workspace=None, stream=None):
+    """Exact attention of each request's new tokens over its paged cache
+    (fa_fwd_paged): prefill chunks, decoding, or both in one batch.
+
+    q: [total_q, H, D] fp16 or bf16, request b's new tokens in rows cu_q[b] ..
+    cu_q[b + 1] (int32 [B + 1]); k_cache, v_cache: [pages, page_size, H_kv, D],
+    any strides, page_size 16, 32, 64 or a multiple of 128; block_table: int32
+    [B, max_pages]; kv_lens: int32 [B], tokens in the cache with the new ones.
+    Causal and window positions count to the end of the request.  ``scale``
+    defaults to 1/sqrt(D).  The workspace is allocated here unless given (a
+    uint8 CUDA tensor of fa_paged_workspace_bytes(D), 256-byte aligned).
+    Returns (out [total_q, H, D], lse float32 [total_q, H] or None); rows no
+    request owns are not written."""
+    import torch
+
+    if q.dim() != 3 or q.stride(2) != 1:
+        raise ValueError("q must be [total_q, H, D], contiguous along D")
+    T, H, D = q.shape
+    dtype = _16bit(q)
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache, v_cache must be [pages, page_size, H_kv, D]")
+    H_kv = k_cache.shape[2]
+    pages, page_size, sp, st_, sh = _cache_layout(k_cache, v_cache, H_kv, D, q.dtype)
+    B = kv_lens.shape[0]
+    _vector("kv_lens", kv_lens, torch.int32, B)
+    _vector("cu_q", cu_q, torch.int32, B + 1)
+    if block_table.dim() != 2 or block_table.dtype != torch.int32 or block_table.shape[0] != B \
+            or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError("block_table must be int32 [B, max_pages], contiguous along the pages")
+    dev = q.device.index
+    _same_device(dev, q=q, k_cache=k_cache, v_cache=v_cache, block_table=block_table, cu_q=cu_q,
+                 kv_lens=kv_lens, out=out, lse=lse, workspace=workspace)
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    if out is None:
+        out = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
+    elif tuple(out.shape) != (T, H, D) or out.dtype != q.dtype or out.stride(2) != 1:
+        raise ValueError("out must be like q, contiguous along D")
+    if not return_lse:
+        lse = None
+    elif lse is None:
+        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
+    elif tuple(lse.shape) != (T, H) or lse.dtype != torch.float32 or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous float32 [total_q, H]")
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    with _on(dev):
+        if workspace is None:
+            workspace = torch.empty(max(fa_paged_workspace_bytes(D), 1), dtype=torch.uint8,
+                                    device=q.device)
+        max_pages = block_table.shape[1]
+        st = fa_fwd_paged(q.data_ptr(), q.stride(0), q.stride(1), k_cache.data_ptr(),
+                          v_cache.data_ptr(), sp, st_, sh, block_table.data_ptr(),
+                          block_table.stride(0) if B > 1 else max_pages, cu_q.data_ptr(),
+                          kv_lens.data_ptr(), out.data_ptr(), out.stride(0), out.stride(1),
+                          lse.data_ptr() if lse is not None else None, T, B, H, H_kv, D, pages,
+                          page_size, max_pages, scale, causal, window_left, window_right, dtype,
+                          workspace.data_ptr(), workspace.numel(), stream.cuda_stream)
+    if st != FA_OK:
+        raise FaError(st, "fa_fwd_paged")
     return out, lse

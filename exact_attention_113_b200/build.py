@@ -8,6 +8,7 @@ through cudaGetDriverEntryPoint, so it loads on a machine without a GPU.
 """
 from __future__ import annotations
 
+import concurrent.futures
 import os
 import re
 import subprocess
@@ -19,18 +20,23 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_DIR = os.path.join(PKG, "lib")
 LIB_PATH = os.path.join(LIB_DIR, "libfa.so")
-SOURCES = [os.path.join(CSRC, "fa_api.cu")]
+# translation units, compiled at the same time: training and contiguous
+# decoding; paged serving
+SOURCES = [os.path.join(CSRC, "fa_api.cu"), os.path.join(CSRC, "fa_paged_api.cu")]
 DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in ("sm100.cuh", "fa_fwd_kernel.cuh",
                                                      "fa_bwd_kernel.cuh",
-                                                     "fa_decode_kernel.cuh")] + [
+                                                     "fa_decode_kernel.cuh",
+                                                     "fa_paged_kernel.cuh",
+                                                     "fa_plan_kernel.cuh",
+                                                     "fa_rope_kernel.cuh")] + [
     os.path.join(INCLUDE, "fa.h")]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17",
-    "-Xcompiler", "-fPIC", "-shared",
-    "-cudart", "static",
+    "-Xcompiler", "-fPIC",
 ]
+LINK_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-cudart", "static"]
 
 
 def nvcc() -> str:
@@ -51,6 +57,8 @@ def is_stale(path: str = LIB_PATH) -> bool:
 # 56 = 512 x 128).  A split is only valid when every instance is compiled at
 # exactly its launch allocation (registers per thread).
 LAUNCH_REGS = {"fa_fwd_kernel": 168, "fa_bwd_kernel": 128}
+# the paged forward's split is the forward's
+PAGED_LAUNCH_REGS = {"fa_paged_kernel": 168}
 
 
 def launch_regs(name: str, tag: str) -> int:
@@ -60,12 +68,12 @@ def launch_regs(name: str, tag: str) -> int:
         m = re.search(r"fa_bwd_kernelILi(\d+)E", name)
         if m and int(m.group(1)) <= 64:
             return 80
-    return LAUNCH_REGS[tag]
+    return {**LAUNCH_REGS, **PAGED_LAUNCH_REGS}[tag]
 
 
-def check_register_counts(ptxas_log: str) -> dict:
-    """Parse `ptxas -v` output; require LAUNCH_REGS for every instance of
-    each setmaxnreg kernel (forward and backward)."""
+def check_register_counts(ptxas_log: str, want: dict = LAUNCH_REGS) -> dict:
+    """Parse `ptxas -v` output; require `want` for every instance of each
+    setmaxnreg kernel (by default the forward's and the backward's)."""
     counts, current = {}, None
     for line in ptxas_log.splitlines():
         m = re.search(r"Function properties for (\S+)", line)
@@ -77,16 +85,16 @@ def check_register_counts(ptxas_log: str) -> dict:
             current = m.group(1)
             continue
         m = re.search(r"Used (\d+) registers", line)
-        if m and current and any(tag in current for tag in LAUNCH_REGS):
+        if m and current and any(tag in current for tag in want):
             counts[current] = int(m.group(1))
-    for tag in LAUNCH_REGS:
+    for tag in want:
         if not any(tag in k for k in counts):
             raise RuntimeError(f"no register counts found for {tag}")
     bad = {k: v for k, v in counts.items()
-           for tag in LAUNCH_REGS if tag in k and v != launch_regs(k, tag)}
+           for tag in want if tag in k and v != launch_regs(k, tag)}
     if bad:
         raise RuntimeError(f"register counts differ from the launch allocation "
-                           f"{LAUNCH_REGS}: {bad}; the setmaxnreg split would not match")
+                           f"{want}: {bad}; the setmaxnreg split would not match")
     return counts
 
 
@@ -103,20 +111,34 @@ def build(force: bool = False, verbose: bool = False, testhooks: bool = False) -
         return path
     os.makedirs(LIB_DIR, exist_ok=True)
     tmp = path + f".tmp{os.getpid()}"
-    cmd = [nvcc(), "-Xptxas=-v", *NVCC_FLAGS, *(TESTHOOKS_FLAGS if testhooks else []),
-           "-I", INCLUDE, "-I", CSRC, "-o", tmp, *SOURCES]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        sys.stderr.write(res.stdout + res.stderr)
-        raise RuntimeError("nvcc failed building libfa.so")
-    if verbose:
-        sys.stderr.write(res.stdout + res.stderr)
+    sources = SOURCES[:1] if testhooks else SOURCES
+    objects = [f"{tmp}.{i}.o" for i in range(len(sources))]
+
+    def run(cmd):
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        if res.returncode != 0:
+            sys.stderr.write(res.stdout + res.stderr)
+            raise RuntimeError("nvcc failed building libfa.so")
+        if verbose:
+            sys.stderr.write(res.stdout + res.stderr)
+        return res.stdout + res.stderr
+
+    def compile_one(src, obj):
+        return run([nvcc(), "-Xptxas=-v", *NVCC_FLAGS, *(TESTHOOKS_FLAGS if testhooks else []),
+                    "-I", INCLUDE, "-I", CSRC, "-c", "-o", obj, src])
+
     try:
-        check_register_counts(res.stdout + res.stderr)
-    except RuntimeError:
-        os.remove(tmp)
-        raise
-    os.replace(tmp, path)
+        with concurrent.futures.ThreadPoolExecutor(len(sources)) as pool:
+            logs = list(pool.map(compile_one, sources, objects))
+        check_register_counts(logs[0])
+        if not testhooks:
+            check_register_counts(logs[1], PAGED_LAUNCH_REGS)
+        run([nvcc(), *LINK_FLAGS, "-o", tmp, *objects])
+        os.replace(tmp, path)
+    finally:
+        for f in objects + [tmp]:
+            if os.path.exists(f):
+                os.remove(f)
     return path
 
 

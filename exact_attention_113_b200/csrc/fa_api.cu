@@ -23,7 +23,7 @@
 namespace fa {
 namespace {
 
-constexpr int kVersion = 10000;  // 1.0.0
+constexpr int kVersion = 10100;  // 1.1.0
 constexpr int kMaxSeq = 1 << 30;
 constexpr int kMaxSplits = 64;
 
@@ -1359,6 +1359,10 @@ extern "C" int fa_test_set_withhold(int block) {
 }
 #endif
 
+namespace fa {
+int paged_take_status();   // fa_paged_api.cu: its own status word
+}
+
 extern "C" int fa_get_device_status(cudaStream_t stream) {
   if (cudaStreamSynchronize(stream) != cudaSuccess) return FA_ERR_CUDA;
   unsigned int st = 0;
@@ -1367,9 +1371,13 @@ extern "C" int fa_get_device_status(cudaStream_t stream) {
     const unsigned int zero = 0;
     if (cudaMemcpyToSymbol(g_fa_status, &zero, sizeof(zero)) != cudaSuccess)
       return FA_ERR_CUDA;
-    return FA_ERR_TIMEOUT;
   }
-  return FA_OK;
+#ifndef FA_TEST_HOOKS   // the watchdog test library is built without that unit
+  const int paged = paged_take_status();
+  if (paged < 0) return FA_ERR_CUDA;
+  st |= static_cast<unsigned int>(paged);
+#endif
+  return st != 0 ? FA_ERR_TIMEOUT : FA_OK;
 }
 
 extern "C" const char *fa_status_string(int status) {

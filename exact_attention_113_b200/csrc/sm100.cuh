@@ -14,9 +14,9 @@
 
 namespace fa {
 
-// Device status word: bit 0 = a bounded wait gave up.  This header is
-// compiled into exactly one translation unit (fa_api.cu), which owns it.
-__device__ unsigned int g_fa_status = 0u;
+// Device status word: bit 0 = a bounded wait gave up.  Each translation unit
+// (fa_api.cu, fa_paged_api.cu) has its own; fa_get_device_status() reads all.
+static __device__ unsigned int g_fa_status = 0u;
 
 // Wait limit: 1 s in the library; the watchdog test library is built with a
 // shorter one (FA_WAIT_LIMIT_NS) so that its withheld-copy test ends quickly.

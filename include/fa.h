@@ -1,5 +1,5 @@
 /*
- * fa.h -- C ABI of the B200 (sm_100a) exact attention forward library
+ * fa.h -- C ABI of the B200 (sm_100a) exact attention library
  *         (libfa.so).
  *
  * The operation: O = softmax(scale * Q K^T + mask) V for every (batch, head),
@@ -350,6 +350,171 @@ int fa_fwd_splitkv_static(const void *q, const void *k, const void *v, void *out
                           float *lse, int B, int H, int H_kv, int L_q, int L_k, int D,
                           float scale, int causal, int window_left, int window_right,
                           int dtype, int n_splits, cudaStream_t stream);
+
+/*
+ * ---------------------------------------------------------------- serving
+ * The entries below run one step of a serving engine around the attention:
+ * fa_paged_plan builds the step's page tables from the request lengths,
+ * fa_qk_norm_rope normalises and rotates q and k and writes k and v into
+ * the paged cache, fa_fwd_paged attends over it.  fa_qk_norm_rope also has
+ * the layouts that fa_fwd / fa_bwd train with, and fa_qk_norm_rope_bwd is
+ * its gradient.  The pages have no counterpart.
+ *
+ * The paged cache: num_pages pages of page_size tokens of H_kv heads of D
+ * values.  Element (page, row, head, d) lies at page * cache_stride_page +
+ * row * cache_stride_token + head * cache_stride_head + d (element strides,
+ * multiples of 8; k and v have the same), so [page, token, head, D] and
+ * [page, head, token, D] both fit.  Slot s is row s % page_size of page
+ * s / page_size.  Token x of request b lies in slot
+ * block_table[b * table_stride + x / page_size] * page_size + x % page_size.
+ */
+
+/*
+ * fa_paged_plan -- one step's page tables, in one launch.
+ *
+ *   q_lens, ctx_lens  device int [B]: new tokens of each request, and tokens
+ *                it has in the cache already (negative: 0)
+ *   block_table  device int [B, table_stride], its first max_pages columns:
+ *                on entry the pages of the tokens in the cache; new entries
+ *                are written behind them, the others stay
+ *   free_pages   device int [n_free]: pages that are handed out, from index
+ *                0, to request 0 first
+ *   cu_q         device int [B + 1] written: 0 and the running sums of q_lens
+ *   kv_lens      device int [B] written: ctx_lens + q_lens
+ *   positions    device int [num_tokens] written: token cu_q[b] + i has
+ *                position ctx_lens[b] + i; -1 behind the last request
+ *   slots        device long long [num_tokens] written: the token's cache
+ *                slot, or -1 (behind the last request, or no page)
+ *   counts       device int [3] written: new tokens in all, pages taken,
+ *                new tokens without a slot (the free list ran out, whose
+ *                table entries get -1, or the table's columns)
+ * num_tokens is the capacity of positions and slots: a padded batch of a
+ * captured graph has more than the requests' tokens, and tokens beyond it
+ * are not written.  FA_ERR_ARG for page_size < 1 or table_stride <
+ * max_pages; pointers to arrays with no elements may be NULL.
+ */
+int fa_paged_plan(const int *q_lens, const int *ctx_lens, int *block_table,
+                  long long table_stride, const int *free_pages, int n_free, int B, int max_pages,
+                  int page_size, int num_tokens, int *cu_q, int *kv_lens, int *positions,
+                  long long *slots, int *counts, cudaStream_t stream);
+
+/* Rows of heads: element (b, l, h, d) at ptr + b * stride_b + l * stride_l +
+ * h * stride_h + d, element strides that are positive multiples of 8 (any
+ * value for an axis of one element), ptr 16-byte aligned. */
+typedef struct {
+    void *ptr;
+    long long stride_b, stride_l, stride_h;
+} fa_rows;
+
+typedef struct {
+    fa_rows q, k, v;          /* [B, L, H, D], [B, L, H_kv, D], [B, L, H_kv, D] */
+    fa_rows q_out, k_out;     /* as q, k; the backward: the gradients of the outputs */
+    const void *q_weight;     /* [D] of `dtype`, 16-byte aligned; NULL: no norm */
+    const void *k_weight;
+    const float *cos_sin;     /* [max_pos, rot_dim]: rot_dim/2 cosines, then the sines */
+    const void *positions;    /* int or long long; (b, l) at b * stride_b + l * stride_l */
+    long long positions_stride_b, positions_stride_l;   /* any, 0 broadcasts */
+    void *k_cache, *v_cache;  /* the paged cache, or NULL */
+    long long cache_stride_page, cache_stride_token, cache_stride_head;
+    const long long *slots;   /* [B * L] contiguous */
+    int num_pages, page_size; /* page_size >= 1 */
+    int positions_64;         /* 0: int, 1: long long */
+    int B, L, H, H_kv, D;     /* H_kv may be 0 */
+    int rot_dim;              /* multiple of 16, 0 .. D */
+    int max_pos;              /* rows of cos_sin */
+    int interleaved;          /* pairs (2i, 2i+1); 0: (i, i + rot_dim/2) */
+    int dtype;
+    float eps;
+} fa_rope_args;
+
+/*
+ * fa_qk_norm_rope -- for every head x of q and k, in one pass:
+ *     y = R(weight .* x / sqrt(mean(x^2) + eps)),
+ * where R turns the first rot_dim values by the token's position p: the pair
+ * (u, w) becomes (u cos - w sin, w cos + u sin) with row p of cos_sin.  All
+ * in fp32, rounded once.  y goes to q_out / k_out and, with a cache, k's y
+ * and v unchanged go to the token's slot (k_out may then be NULL).  q_out may
+ * be q itself, k_out k itself; no other overlap.  No two tokens may have the
+ * same slot.
+ *
+ * A token whose position is negative or >= max_pos is padding: nothing of it
+ * is written.  A token whose slot is negative or >= num_pages * page_size
+ * writes no cache.  L == 0 is a no-op.
+ * Errors: FA_ERR_ARG for a bad rot_dim, eps, page_size or num_pages;
+ * FA_ERR_ALIGN for a misaligned pointer or stride; others as fa_fwd.
+ */
+int fa_qk_norm_rope(const fa_rope_args *args, cudaStream_t stream);
+
+/* Workspace bytes of fa_qk_norm_rope_bwd on the current device (0 for an
+ * unsupported D): one fp32 row of D per block. */
+size_t fa_qk_norm_rope_bwd_workspace_bytes(int D);
+
+/*
+ * fa_qk_norm_rope_bwd -- the gradients of sum(q_out .* dq_out) + sum(k_out .*
+ * dk_out) for the outputs of fa_qk_norm_rope: args->q and k are its inputs,
+ * args->q_out and k_out hold dq_out and dk_out (read); v and the cache are
+ * not used.  Written:
+ *   dq, dk       as q, k (RNE of fp32); zero for padding tokens
+ *   dq_weight, dk_weight  device fp32 [D], given exactly where the weight is:
+ *                sum over all rows of R^T(dy) .* x / sqrt(mean(x^2) + eps),
+ *                in a fixed order (the same bits every time on one device)
+ *   workspace    device, 256-byte aligned, at least
+ *                fa_qk_norm_rope_bwd_workspace_bytes(D) bytes; contents on
+ *                entry do not matter; not needed without weights.  Calls that
+ *                share a workspace must not overlap on the GPU.
+ * dq may be dq_out itself (dk likewise); no other overlap.  L == 0 writes
+ * zero weight gradients.
+ */
+int fa_qk_norm_rope_bwd(const fa_rope_args *args, fa_rows dq, fa_rows dk, float *dq_weight,
+                        float *dk_weight, void *workspace, size_t workspace_bytes,
+                        cudaStream_t stream);
+
+/* Workspace bytes of fa_fwd_paged on the current device (0 for an
+ * unsupported D): two partial tiles of 256 rows for each SM.  They do not
+ * depend on the batch. */
+size_t fa_paged_workspace_bytes(int D);
+
+/*
+ * fa_fwd_paged -- exact attention of each request's new tokens over its
+ * paged key/value cache, which holds the new tokens' keys and values too:
+ * prefill chunks, single tokens (decoding) and mixtures, in two launches.
+ *
+ *   q         device, rows of `dtype`: token t, head h at t * q_stride_t +
+ *             h * q_stride_h; request b's new tokens are cu_q[b] ..
+ *             cu_q[b+1] - 1 of the total_q rows
+ *   k_cache, v_cache, block_table  as above; entries of pages that hold no
+ *             visible key are not used, and an entry that names no page
+ *             reads as zeros
+ *   cu_q, kv_lens  device int [B + 1], [B]: kv_lens[b] tokens are in the
+ *             cache, the last cu_q[b+1] - cu_q[b] of them new
+ *   out       device, as q with its own strides; lse [total_q, H] fp32 or NULL
+ *   causal, window_left, window_right  as fa_fwd, with positions in the
+ *             request: new token i is at kv_len - q_len + i, and key j is
+ *             visible iff j < kv_len, j <= position + window_right (0 when
+ *             causal), j >= position - window_left
+ *   D         a multiple of 16 in [16, 128]; H / H_kv at most 128
+ *   page_size 16, 32, 64 or a multiple of 128 (FA_ERR_ARG)
+ *   workspace device, 256-byte aligned, at least fa_paged_workspace_bytes(D)
+ *             bytes; contents on entry do not matter.  Calls that share a
+ *             workspace must not overlap on the GPU.
+ * A row that sees no key gets out = 0 and lse = -inf.  Rows of q, out and
+ * lse outside cu_q[0] .. cu_q[B] are neither read into a result nor written.
+ * Cache rows behind kv_len may hold anything, NaN included; a key or value
+ * that some query of a request's 2 * floor(128 / (H / H_kv)) neighbouring
+ * tokens sees has to be finite to leave the others' results finite.
+ * The results do not depend on timing: the same bits for the same lengths.
+ * Lengths live on the device and are not checked on the host: sums that
+ * exceed total_q and lengths that exceed max_pages * page_size are cut.
+ * total_q == 0 is a no-op.  Other errors as fa_fwd.
+ */
+int fa_fwd_paged(const void *q, long long q_stride_t, long long q_stride_h, const void *k_cache,
+                 const void *v_cache, long long cache_stride_page, long long cache_stride_token,
+                 long long cache_stride_head, const int *block_table, long long table_stride,
+                 const int *cu_q, const int *kv_lens, void *out, long long out_stride_t,
+                 long long out_stride_h, float *lse, int total_q, int B, int H, int H_kv, int D,
+                 int num_pages, int page_size, int max_pages, float scale, int causal,
+                 int window_left, int window_right, int dtype, void *workspace,
+                 size_t workspace_bytes, cudaStream_t stream);
 
 /*
  * fa_get_device_status -- synchronise `stream`, then read and clear the
