@@ -21,14 +21,15 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_DIR = os.path.join(PKG, "lib")
 LIB_PATH = os.path.join(LIB_DIR, "libfa.so")
 # translation units, compiled at the same time: training and contiguous
-# decoding; paged serving
-SOURCES = [os.path.join(CSRC, "fa_api.cu"), os.path.join(CSRC, "fa_paged_api.cu")]
+# decoding; attention over a paged cache; page tables, norm and rotation
+SOURCES = [os.path.join(CSRC, f) for f in ("fa_api.cu", "fa_paged_api.cu", "fa_serve_api.cu")]
 DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in ("sm100.cuh", "fa_fwd_kernel.cuh",
                                                      "fa_bwd_kernel.cuh",
                                                      "fa_decode_kernel.cuh",
                                                      "fa_paged_kernel.cuh",
                                                      "fa_plan_kernel.cuh",
-                                                     "fa_rope_kernel.cuh")] + [
+                                                     "fa_rope_kernel.cuh",
+                                                     "fa_serve_host.h")] + [
     os.path.join(INCLUDE, "fa.h")]
 
 NVCC_FLAGS = [

@@ -9,21 +9,29 @@
 //   dx = r (w .* g - x r mean(w .* g .* x r)).
 //
 // Both read and write every value once and do some ten operations on it: HBM
-// bounds them.  A row (one head of one token) belongs to D / 16 lanes, each
-// with two 16-byte vectors that hold whole pairs (8 values from each half, or
-// 16 neighbours), so the rotation needs no exchange and only the norm's sum
-// crosses lanes.  A warp takes one token's rows, kUnroll per lane with all
-// their loads issued first, and reads its cosines and weights once for them.
-// All arithmetic is fp32; the result is rounded once.
+// bounds them, and close behind it the instructions (unpacking 16-bit values,
+// addresses), which is why the arithmetic runs on fp32 pairs.  A row (one head
+// of one token) belongs to D / 16 lanes, each with two 16-byte vectors that
+// hold whole pairs (8 values from each half, or 16 neighbours), so the rotation
+// needs no exchange and only the norm's sum crosses lanes.  Rows are copied to
+// shared memory some steps ahead.  All arithmetic is fp32; the result is
+// rounded once.  Measured: forward 0.90 of the HBM copy rate at B4 L8192 H48
+// D64 (137 us), gradient 0.78 at B2 L16384 H32/8 D128 (200 us).
 #pragma once
 
 #include "sm100.cuh"
 
 namespace fa {
 
+// Stages and blocks per SM, measured on 8192 tokens (48 rows of D 128 each) and
+// on B4 L8192 H48 D64: 4 stages, 4 blocks 51 / 137 us; 5 blocks (fewer
+// registers) 53 / 142; 3 stages 51 / 141.  The gradient at B2 L16384 H32/8
+// D128: 3 stages, 4 blocks 200 us; 2 stages 208; 4 stages 210.
 constexpr int kRopeThreads = 128;
-constexpr int kRopeUnroll = 4;
-constexpr int kRopeBwdThreads = 256;
+constexpr int kRopeStages = 4;        // rows a lane has in shared memory
+constexpr int kRopeBlocks = 4;        // resident per SM
+constexpr int kRopeBwdStages = 3;
+constexpr int kRopeBwdBlocks = 4;
 
 struct RopeView {
   const uint8_t *ptr;
@@ -44,13 +52,15 @@ struct RopeParams {
   long long n_slots;
   int page_size;
   int B, L, H, H_kv, D, rot, max_pos, interleaved;
-  float eps;
+  float eps, inv_d;
   // backward
   RopeView dyq, dyk;      // gradients of the outputs
   RopeView dq, dk;        // written
   float *part;            // [blocks][D] partial weight gradients
   float *dwq, *dwk;       // [D]
-  int blocks_q, blocks_k;
+  int blocks_q, blocks_k;     // blocks of query rows, key rows (the rest: value rows)
+  int chunks_q, chunks_k;     // chunks of a token's rows
+  int per_q, per_k;           // steps of a chunk
 };
 
 // This lane's place in a row of D values: two vectors of 8 and whether they
@@ -82,39 +92,60 @@ __device__ __forceinline__ float2 unpack2(uint32_t v) {
     return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&v));
 }
 
+// A lane's 16 values as fp32 pairs: x[0..3] the first vector, x[4..7] the
+// second.  The arithmetic runs on pairs (one instruction for two values).
+struct Row16 {
+  float2 x[8];
+};
 template <int DT>
-__device__ __forceinline__ void unpack16(const uint4 &a, const uint4 &b, float (&x)[16]) {
+__device__ __forceinline__ Row16 unpack16(const uint4 &a, const uint4 &b) {
   const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  Row16 r;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float2 f = unpack2<DT>(w[i]);
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
-  }
+  for (int i = 0; i < 8; ++i) r.x[i] = unpack2<DT>(w[i]);
+  return r;
 }
 template <int DT>
-__device__ __forceinline__ void pack16(const float (&x)[16], uint4 &a, uint4 &b) {
-  a = make_uint4(pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3]), pack2<DT>(x[4], x[5]),
-                 pack2<DT>(x[6], x[7]));
-  b = make_uint4(pack2<DT>(x[8], x[9]), pack2<DT>(x[10], x[11]), pack2<DT>(x[12], x[13]),
-                 pack2<DT>(x[14], x[15]));
+__device__ __forceinline__ void pack16(const Row16 &r, uint4 &a, uint4 &b) {
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = pack2<DT>(r.x[i].x, r.x[i].y);
+  a = make_uint4(w[0], w[1], w[2], w[3]);
+  b = make_uint4(w[4], w[5], w[6], w[7]);
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// sum of x .* y over the lane's 16 values
+__device__ __forceinline__ float dot16(const Row16 &x, const Row16 &y) {
+  float2 s[2] = {both(0.0f), both(0.0f)};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s[i & 1] = __ffma2_rn(x.x[i], y.x[i], s[i & 1]);
+  return (s[0].x + s[1].x) + (s[0].y + s[1].y);
 }
 
-// The lane's 8 pairs turned by +angle (kSign 1) or -angle (kSign -1).
-template <int kSign>
-__device__ __forceinline__ void turn16(float (&x)[16], const float (&c)[8], const float (&s)[8],
-                                       int interleaved) {
+// The lane's 8 pairs turned by +angle (kSign 1) or -angle (kSign -1); c, s:
+// its 8 cosines and sines.
+template <int kSign, bool kInter>
+__device__ __forceinline__ void turn16(Row16 &r, const float4 (&c)[2], const float4 (&s)[2]) {
+  const float2 cc[4] = {make_float2(c[0].x, c[0].y), make_float2(c[0].z, c[0].w),
+                        make_float2(c[1].x, c[1].y), make_float2(c[1].z, c[1].w)};
+  const float2 ss[4] = {make_float2(s[0].x, s[0].y), make_float2(s[0].z, s[0].w),
+                        make_float2(s[1].x, s[1].y), make_float2(s[1].z, s[1].w)};
+  if constexpr (kInter) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float si = kSign * s[i];
-    if (interleaved) {
-      const float a = x[2 * i], b = x[2 * i + 1];
-      x[2 * i] = a * c[i] - b * si;
-      x[2 * i + 1] = b * c[i] + a * si;
-    } else {
-      const float a = x[i], b = x[8 + i];
-      x[i] = a * c[i] - b * si;
-      x[8 + i] = b * c[i] + a * si;
+    for (int i = 0; i < 8; ++i) {
+      const float ci = i & 1 ? cc[i >> 1].y : cc[i >> 1].x;
+      const float si = kSign * (i & 1 ? ss[i >> 1].y : ss[i >> 1].x);
+      const float2 v = r.x[i];
+      r.x[i] = __ffma2_rn(v, both(ci), __fmul2_rn(make_float2(v.y, v.x), make_float2(-si, si)));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 a = r.x[i], b = r.x[4 + i];
+      const float2 p = make_float2(kSign * ss[i].x, kSign * ss[i].y), n = make_float2(-p.x, -p.y);
+      r.x[i] = __ffma2_rn(a, cc[i], __fmul2_rn(b, n));
+      r.x[4 + i] = __ffma2_rn(b, cc[i], __fmul2_rn(a, p));
     }
   }
 }
@@ -132,244 +163,353 @@ __device__ __forceinline__ long long rope_position(const RopeParams &p, int b, i
                  : static_cast<long long>(__ldg(static_cast<const int *>(p.pos) + at));
 }
 
+// The lane's cosines and sines (the first reading of a row of the table comes
+// from L2, the warp's others from L1, so they are not kept in registers).
 __device__ __forceinline__ void rope_angles(const RopeParams &p, long long pos, const RopeLane &w,
-                                            float (&c)[8], float (&s)[8]) {
-  if (w.turn) {
-    const float4 *row = reinterpret_cast<const float4 *>(p.cos_sin + pos * p.rot + w.i0);
-    const float4 c0 = __ldg(row), c1 = __ldg(row + 1);
-    const float4 *rs = reinterpret_cast<const float4 *>(p.cos_sin + pos * p.rot + p.rot / 2 + w.i0);
-    const float4 s0 = __ldg(rs), s1 = __ldg(rs + 1);
-    c[0] = c0.x; c[1] = c0.y; c[2] = c0.z; c[3] = c0.w;
-    c[4] = c1.x; c[5] = c1.y; c[6] = c1.z; c[7] = c1.w;
-    s[0] = s0.x; s[1] = s0.y; s[2] = s0.z; s[3] = s0.w;
-    s[4] = s1.x; s[5] = s1.y; s[6] = s1.z; s[7] = s1.w;
+                                            float4 (&c)[2], float4 (&s)[2]) {
+  const float4 *row = reinterpret_cast<const float4 *>(p.cos_sin + pos * p.rot + w.i0);
+  const float4 *rs = reinterpret_cast<const float4 *>(p.cos_sin + pos * p.rot + p.rot / 2 + w.i0);
+  c[0] = __ldg(row);
+  c[1] = __ldg(row + 1);
+  s[0] = __ldg(rs);
+  s[1] = __ldg(rs + 1);
+}
+template <int DT>
+__device__ __forceinline__ Row16 rope_weight(const void *weight, const RopeLane &w) {
+  const uint8_t *at = static_cast<const uint8_t *>(weight);
+  return unpack16<DT>(__ldg(reinterpret_cast<const uint4 *>(at + 2 * w.a)),
+                      __ldg(reinterpret_cast<const uint4 *>(at + 2 * w.b)));
+}
+
+__device__ __forceinline__ void st16(uint8_t *p, const uint4 &v) { *reinterpret_cast<uint4 *>(p) = v; }
+
+// 16 bytes into the lane's own place in shared memory, asynchronously; zeros
+// where !ok (nothing is read then).
+__device__ __forceinline__ void copy16(uint4 *dst, const uint8_t *src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(ok ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+
+// A warp's walk over the rows of its kind.  A token's rows are `steps` steps
+// of 32 / kSeg rows, one a lane segment.
+struct RopeWalk {
+  int b, l, r;        // batch, token, step within the token
+  bool fresh;         // another token, or another run of its steps, has begun
+  __device__ __forceinline__ uint8_t *row(const RopeView &v, int h) const {
+    return const_cast<uint8_t *>(v.ptr) + 2 * (b * v.sb + l * v.sl + h * v.sh);
   }
-}
+};
 
-__device__ __forceinline__ uint4 ld16(const uint8_t *base, long long elem) {
-  return *reinterpret_cast<const uint4 *>(base + 2 * elem);
-}
-__device__ __forceinline__ void st16(const uint8_t *base, long long elem, const uint4 &v) {
-  *reinterpret_cast<uint4 *>(const_cast<uint8_t *>(base) + 2 * elem) = v;
-}
-
-// kSeg lanes a row: the smallest power of two >= D / 16.  Rows of a token:
-// H query heads, H_kv key heads and, for the cache, H_kv value heads (copied).
-template <int kSeg, int DT>
-__global__ void __launch_bounds__(kRopeThreads) fa_rope_fwd_kernel(const __grid_constant__ RopeParams p) {
-  constexpr int kRowsWarp = 32 / kSeg;
-  constexpr int kChunk = kRowsWarp * kRopeUnroll;   // rows a warp takes
-  const int lane = threadIdx.x & 31;
-  const int rows = p.H + p.H_kv + (p.vc ? p.H_kv : 0);
-  const int chunks = (rows + kChunk - 1) / kChunk;
-  const long long item = static_cast<long long>(blockIdx.x) * (kRopeThreads / 32) + (threadIdx.x >> 5);
-  if (item >= static_cast<long long>(p.B) * p.L * chunks) return;
-  const long long token = item / chunks;
-  const int row0 = static_cast<int>(item - token * chunks) * kChunk + lane / kSeg;
-  const int b = static_cast<int>(token / p.L), l = static_cast<int>(token - static_cast<long long>(b) * p.L);
-  const RopeLane w = rope_lane(lane % kSeg, p.D, p.rot, p.interleaved);
-
-  // all loads of the lane first
-  uint4 xa[kRopeUnroll], xb[kRopeUnroll];
-#pragma unroll
-  for (int i = 0; i < kRopeUnroll; ++i) {
-    const int row = row0 + i * kRowsWarp;
-    xa[i] = xb[i] = make_uint4(0, 0, 0, 0);
-    if (w.on && row < rows) {
-      const RopeView &in = row < p.H ? p.q : (row < p.H + p.H_kv ? p.k : p.v);
-      const int h = row < p.H ? row : (row < p.H + p.H_kv ? row - p.H : row - p.H - p.H_kv);
-      const long long at = b * in.sb + l * in.sl + h * in.sh;
-      // (value heads are copied: neighbouring vectors, whatever the pairs are)
-      const bool copy = row >= p.H + p.H_kv;
-      const int s = lane % kSeg;
-      xa[i] = ld16(in.ptr, at + (copy ? 16 * s : w.a));
-      xb[i] = ld16(in.ptr, at + (copy ? 16 * s + 8 : w.b));
+// Every n-th chunk of at most `per` steps: the warps that run together work on
+// neighbouring tokens, whose rows of one head are neighbours in a
+// [B, H, L, D] output (the forward at B4 L8192 H48 D64: 139 us, in runs 162).
+struct RopeChunks : RopeWalk {
+  unsigned item, items, n;
+  int steps, chunks, per, end;
+  __device__ __forceinline__ void start(const RopeParams &p, bool is_q, unsigned me, unsigned warps,
+                                        int steps_) {
+    steps = steps_;
+    chunks = is_q ? p.chunks_q : p.chunks_k;
+    per = is_q ? p.per_q : p.per_k;
+    item = me;
+    items = p.B * p.L * chunks;
+    n = warps;
+    locate(p);
+  }
+  __device__ __forceinline__ void locate(const RopeParams &p) {
+    const unsigned token = chunks == 1 ? item : item / chunks;
+    r = chunks == 1 ? 0 : (item - token * chunks) * per;
+    end = min(r + per, steps);
+    b = p.B == 1 ? 0 : token / p.L;
+    l = token - b * p.L;
+    fresh = true;
+  }
+  __device__ __forceinline__ bool more() const { return item < items; }
+  __device__ __forceinline__ void next(const RopeParams &p) {
+    fresh = false;
+    if (++r == end) {
+      item += n;
+      locate(p);
     }
   }
-  const long long pos = rope_position(p, b, l);
-  if (pos < 0 || pos >= p.max_pos) return;   // padding: left as it was
-  long long cache = -1;
-  if (p.kc) {
-    const long long slot = __ldg(p.slots + token);
-    if (slot >= 0 && slot < p.n_slots)
-      cache = slot / p.page_size * p.c_sp + slot % p.page_size * p.c_st;
+};
+
+// An equal run of steps for each warp, tokens in order: the fewest
+// instructions (the gradient at B2 L16384 H32/8 D128: 202 us, in chunks 230).
+struct RopeRun : RopeWalk {
+  unsigned at, to;
+  int steps;
+  __device__ __forceinline__ void start(const RopeParams &p, bool, unsigned me, unsigned warps,
+                                        int steps_) {
+    steps = steps_;
+    const unsigned total = p.B * p.L * steps, q = total / warps, rest = total % warps;
+    at = q * me + min(me, rest);
+    to = at + q + (me < rest ? 1 : 0);
+    const unsigned token = at / steps;
+    r = at - token * steps;
+    b = p.B == 1 ? 0 : token / p.L;
+    l = token - b * p.L;
+    fresh = true;
   }
-  float c[8], s[8];
-  rope_angles(p, pos, w, c, s);
-  uint4 wqa = make_uint4(0, 0, 0, 0), wqb = wqa, wka = wqa, wkb = wqa;
-  if (w.on && p.wq) {
-    wqa = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p.wq) + 2 * w.a));
-    wqb = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p.wq) + 2 * w.b));
-  }
-  if (w.on && p.wk) {
-    wka = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p.wk) + 2 * w.a));
-    wkb = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p.wk) + 2 * w.b));
-  }
-#pragma unroll
-  for (int i = 0; i < kRopeUnroll; ++i) {
-    const int row = row0 + i * kRowsWarp;
-    const bool is_q = row < p.H, copy = row >= p.H + p.H_kv;
-    float x[16];
-    unpack16<DT>(xa[i], xb[i], x);
-    float ss = 0.0f;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) ss += x[e] * x[e];
-    ss = seg_sum<kSeg>(ss);
-    if (!w.on || row >= rows) continue;
-    const int h = is_q ? row : (copy ? row - p.H - p.H_kv : row - p.H);
-    if (copy) {
-      if (cache >= 0) {
-        const int s0 = 16 * (lane % kSeg);
-        st16(p.vc, cache + h * p.c_sh + s0, xa[i]);
-        st16(p.vc, cache + h * p.c_sh + s0 + 8, xb[i]);
+  __device__ __forceinline__ bool more() const { return at < to; }
+  __device__ __forceinline__ void next(const RopeParams &p) {
+    ++at;
+    fresh = ++r == steps;
+    if (fresh) {
+      r = 0;
+      if (++l == p.L) {
+        l = 0;
+        ++b;
       }
-      continue;
     }
-    if (is_q ? p.wq != nullptr : p.wk != nullptr) {
-      const float r = 1.0f / sqrtf(ss / p.D + p.eps);
-      float g[16];
-      unpack16<DT>(is_q ? wqa : wka, is_q ? wqb : wkb, g);
+  }
+};
+
+// kSeg lanes a row: the smallest power of two >= D / 16.  Blocks are dealt to
+// the kinds of rows (query, key, and value rows, which only move to the cache)
+// in proportion, and a kind's chunks to its warps.  A lane has its next kRopeStages - 1 rows under way in shared memory, where no registers
+// wait for them and, as it reads only what it copied itself, no barrier either.
+template <int kSeg, int DT, bool kInter>
+__global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
+    fa_rope_fwd_kernel(const __grid_constant__ RopeParams p) {
+  constexpr int kRowsWarp = 32 / kSeg, S = kRopeStages, kWarps = kRopeThreads / 32;
+  __shared__ uint4 ring[kWarps][S][2][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, s = lane % kSeg;
+  const int bid = blockIdx.x;
+  const bool is_q = bid < p.blocks_q, is_v = bid >= p.blocks_q + p.blocks_k;
+  const int blocks = is_q ? p.blocks_q : (is_v ? gridDim.x - p.blocks_q - p.blocks_k : p.blocks_k);
+  const unsigned me = (bid - (is_q ? 0 : (is_v ? p.blocks_q + p.blocks_k : p.blocks_q))) * kWarps + warp;
+  const int H = is_q ? p.H : p.H_kv;
+  const int steps = (H + kRowsWarp - 1) / kRowsWarp;
+  const RopeView in = is_q ? p.q : (is_v ? p.v : p.k), out = is_q ? p.qo : p.ko;
+  RopeLane w = rope_lane(s, p.D, p.rot, kInter);
+  if (is_v) {   // copied: neighbouring vectors, whatever the pairs are
+    w.a = 16 * s;
+    w.b = 16 * s + 8;
+  }
+  const int ab = 2 * (w.b - w.a), hl = lane / kSeg;
+  const void *weight = is_v ? nullptr : (is_q ? p.wq : p.wk);
+  Row16 g;
+  if (w.on && weight) g = rope_weight<DT>(weight, w);
+
+  RopeChunks fw, cw;
+  fw.start(p, is_q, me, blocks * kWarps, steps);
+  cw = fw;
+  const uint8_t *src = nullptr;
+  auto fetch = [&](int slot) {
+    if (fw.more()) {
+      if (fw.fresh) src = fw.row(in, fw.r * kRowsWarp + hl) + 2 * w.a;
+      const bool ok = w.on && fw.r * kRowsWarp + hl < H;
+      copy16(&ring[warp][slot][0][lane], src, ok);
+      copy16(&ring[warp][slot][1][lane], src + ab, ok);
+      src += 2 * kRowsWarp * in.sh;
+      fw.next(p);
+    }
+    copy_commit();
+  };
 #pragma unroll
-      for (int e = 0; e < 16; ++e) x[e] = x[e] * r * g[e];
+  for (int k = 0; k < S - 1; ++k) fetch(k);
+  int slot = 0;
+  bool real = false, turn = false;
+  uint8_t *d0 = nullptr, *d1 = nullptr;   // where a row goes: the output, the cache
+  float4 co[2], si[2];
+  for (; cw.more(); cw.next(p)) {
+    if (cw.fresh) {
+      const long long pos = rope_position(p, cw.b, cw.l);
+      const int h = cw.r * kRowsWarp + hl;
+      real = pos >= 0 && pos < p.max_pos;   // else padding: left as it was
+      d0 = !is_v && out.ptr ? cw.row(out, h) + 2 * w.a : nullptr;
+      d1 = nullptr;
+      if (!is_q && p.kc) {
+        const long long slot_id = __ldg(p.slots + static_cast<long long>(cw.b) * p.L + cw.l);
+        if (slot_id >= 0 && slot_id < p.n_slots) {
+          long long page, in_page;
+          if (p.n_slots <= 0x7fffffffll) {   // (a 32-bit division is a third of the cost)
+            page = static_cast<unsigned>(slot_id) / static_cast<unsigned>(p.page_size);
+            in_page = static_cast<unsigned>(slot_id) % static_cast<unsigned>(p.page_size);
+          } else {
+            page = slot_id / p.page_size;
+            in_page = slot_id % p.page_size;
+          }
+          d1 = (is_v ? p.vc : p.kc) + 2 * (page * p.c_sp + in_page * p.c_st + h * p.c_sh + w.a);
+        }
+      }
+      turn = w.turn && real && !is_v;
+      if (turn) rope_angles(p, pos, w, co, si);
     }
-    if (w.turn) turn16<1>(x, c, s, p.interleaved);
-    uint4 a, bb;
-    pack16<DT>(x, a, bb);
-    const RopeView &out = is_q ? p.qo : p.ko;
-    if (out.ptr) {
-      const long long at = b * out.sb + l * out.sl + h * out.sh;
-      st16(out.ptr, at + w.a, a);
-      st16(out.ptr, at + w.b, bb);
+    copy_wait<S - 2>();
+    uint4 a = ring[warp][slot][0][lane], bb = ring[warp][slot][1][lane];
+    slot = slot + 1 == S ? 0 : slot + 1;
+    fetch(slot + S - 2 >= S ? slot - 2 : slot + S - 2);   // the slot read one row ago
+    if (!real) continue;
+    if (!is_v) {
+      Row16 x = unpack16<DT>(a, bb);
+      if (weight) {
+        const float2 q = both(rsqrtf(seg_sum<kSeg>(dot16(x, x)) * p.inv_d + p.eps));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x.x[e] = __fmul2_rn(__fmul2_rn(x.x[e], q), g.x[e]);
+      }
+      if (turn) turn16<1, kInter>(x, co, si);
+      pack16<DT>(x, a, bb);
     }
-    if (!is_q && cache >= 0) {
-      st16(p.kc, cache + h * p.c_sh + w.a, a);
-      st16(p.kc, cache + h * p.c_sh + w.b, bb);
+    if (w.on && cw.r * kRowsWarp + hl < H) {
+      if (d0) {
+        st16(d0, a);
+        st16(d0 + ab, bb);
+        d0 += 2 * kRowsWarp * out.sh;
+      }
+      if (d1) {
+        st16(d1, a);
+        st16(d1 + ab, bb);
+        d1 += 2 * kRowsWarp * p.c_sh;
+      }
     }
   }
 }
 
-// Blocks [0, blocks_q) take the query rows, the others the key rows, each
-// block every blocks-th group of tokens: a lane meets the same columns in all
-// its rows and sums its 16 weight gradients in registers; the block adds its
-// lanes in a fixed order and leaves one partial row of D.
-template <int kSeg, int DT>
-__global__ void __launch_bounds__(kRopeBwdThreads) fa_rope_bwd_kernel(const __grid_constant__ RopeParams p) {
-  constexpr int kRowsWarp = 32 / kSeg;
-  constexpr int kWarps = kRopeBwdThreads / 32;
-  constexpr int kUnroll = 2;
-  constexpr int kChunk = kRowsWarp * kUnroll;
-  __shared__ float red[kWarps][kRowsWarp][kSeg * 16];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// The same walk with two rows to a step, x and dy.  A lane meets the same
+// columns in all its rows and sums its 16 weight gradients in registers; the
+// block adds its lanes in a fixed order and leaves one partial row of D.  With
+// t = sum(w g x) the input's gradient is dx = r w g - x r^3 t / D, so the two
+// sums over a row, of x x and of w g x, cross the lanes together.
+template <int kSeg, int DT, bool kInter>
+__global__ void __launch_bounds__(kRopeThreads, kRopeBwdBlocks)
+    fa_rope_bwd_kernel(const __grid_constant__ RopeParams p) {
+  constexpr int kRowsWarp = 32 / kSeg, S = kRopeBwdStages, kWarps = kRopeThreads / 32;
+  __shared__ uint4 ring[kWarps][S][4][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, hl = lane / kSeg;
   const bool is_q = static_cast<int>(blockIdx.x) < p.blocks_q;
-  const int block = is_q ? blockIdx.x : blockIdx.x - p.blocks_q;
-  const int n_blocks = is_q ? p.blocks_q : p.blocks_k;
+  const unsigned me = (is_q ? blockIdx.x : blockIdx.x - p.blocks_q) * kWarps + warp;
+  const unsigned n = (is_q ? p.blocks_q : p.blocks_k) * kWarps;
   const int H = is_q ? p.H : p.H_kv;
+  const int steps = (H + kRowsWarp - 1) / kRowsWarp;
   const RopeView in = is_q ? p.q : p.k, dy = is_q ? p.dyq : p.dyk, dx = is_q ? p.dq : p.dk;
   const void *weight = is_q ? p.wq : p.wk;
-  const int chunks = (H + kChunk - 1) / kChunk;
-  const long long items = static_cast<long long>(p.B) * p.L * chunks;
-  const RopeLane w = rope_lane(lane % kSeg, p.D, p.rot, p.interleaved);
-  float g[16], acc[16];
+  const RopeLane w = rope_lane(lane % kSeg, p.D, p.rot, kInter);
+  const int ab = 2 * (w.b - w.a);
+  Row16 g;
+  float2 acc[8];
 #pragma unroll
-  for (int e = 0; e < 16; ++e) acc[e] = 0.0f, g[e] = 1.0f;
-  if (w.on && weight)
-    unpack16<DT>(__ldg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(weight) + 2 * w.a)),
-                 __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(weight) + 2 * w.b)), g);
-  const float inv_d = 1.0f / p.D;
-  for (long long item = static_cast<long long>(block) * kWarps + warp; item < items;
-       item += static_cast<long long>(n_blocks) * kWarps) {
-    const long long token = item / chunks;
-    const int row0 = static_cast<int>(item - token * chunks) * kChunk + lane / kSeg;
-    const int b = static_cast<int>(token / p.L), l = static_cast<int>(token - static_cast<long long>(b) * p.L);
-    uint4 xa[kUnroll], xb[kUnroll], ya[kUnroll], yb[kUnroll];
-#pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-      const int h = row0 + i * kRowsWarp;
-      xa[i] = xb[i] = ya[i] = yb[i] = make_uint4(0, 0, 0, 0);
-      if (w.on && h < H) {
-        const long long at = b * in.sb + l * in.sl + h * in.sh;
-        const long long ay = b * dy.sb + l * dy.sl + h * dy.sh;
-        xa[i] = ld16(in.ptr, at + w.a);
-        xb[i] = ld16(in.ptr, at + w.b);
-        ya[i] = ld16(dy.ptr, ay + w.a);
-        yb[i] = ld16(dy.ptr, ay + w.b);
+  for (int e = 0; e < 8; ++e) acc[e] = g.x[e] = both(0.0f);
+  if (w.on && weight) g = rope_weight<DT>(weight, w);
+
+  RopeRun fw, cw;
+  fw.start(p, is_q, me, n, steps);
+  cw = fw;
+  const uint8_t *sx = nullptr, *sy = nullptr;
+  auto fetch = [&](int slot) {
+    if (fw.more()) {
+      const int h = fw.r * kRowsWarp + hl;
+      if (fw.fresh) {
+        sx = fw.row(in, h) + 2 * w.a;
+        sy = fw.row(dy, h) + 2 * w.a;
       }
+      const bool ok = w.on && h < H;
+      copy16(&ring[warp][slot][0][lane], sx, ok);
+      copy16(&ring[warp][slot][1][lane], sx + ab, ok);
+      copy16(&ring[warp][slot][2][lane], sy, ok);
+      copy16(&ring[warp][slot][3][lane], sy + ab, ok);
+      sx += 2 * kRowsWarp * in.sh;
+      sy += 2 * kRowsWarp * dy.sh;
+      fw.next(p);
     }
-    const long long pos = rope_position(p, b, l);
-    const bool real = pos >= 0 && pos < p.max_pos;
-    float c[8], s[8];
-    if (real) rope_angles(p, pos, w, c, s);
+    copy_commit();
+  };
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-      const int h = row0 + i * kRowsWarp;
-      float x[16], y[16];
-      unpack16<DT>(xa[i], xb[i], x);
-      unpack16<DT>(ya[i], yb[i], y);
-      if (w.turn && real) turn16<-1>(y, c, s, p.interleaved);
+  for (int k = 0; k < S - 1; ++k) fetch(k);
+  int slot = 0;
+  bool real = false;
+  uint8_t *dst = nullptr;
+  float4 co[2], si[2];
+  for (; cw.more(); cw.next(p)) {
+    if (cw.fresh) {
+      const long long pos = rope_position(p, cw.b, cw.l);
+      real = pos >= 0 && pos < p.max_pos;   // else padding, without an output
+      dst = cw.row(dx, cw.r * kRowsWarp + hl) + 2 * w.a;
+      if (w.turn && real) rope_angles(p, pos, w, co, si);
+    }
+    copy_wait<S - 2>();
+    Row16 x = unpack16<DT>(ring[warp][slot][0][lane], ring[warp][slot][1][lane]);
+    Row16 y = unpack16<DT>(ring[warp][slot][2][lane], ring[warp][slot][3][lane]);
+    slot = slot + 1 == S ? 0 : slot + 1;
+    fetch(slot + S - 2 >= S ? slot - 2 : slot + S - 2);   // the slot read one row ago
+    uint4 a = make_uint4(0, 0, 0, 0), bb = a;
+    if (real) {
+      if (w.turn) turn16<-1, kInter>(y, co, si);
       if (weight) {
-        float ss = 0.0f, dot = 0.0f;
+        Row16 wg;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) ss += x[e] * x[e];
-        const float r = 1.0f / sqrtf(seg_sum<kSeg>(ss) / p.D + p.eps);
+        for (int e = 0; e < 8; ++e) wg.x[e] = __fmul2_rn(y.x[e], g.x[e]);
+        float ss = dot16(x, x), t = dot16(x, wg);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          x[e] *= r;
-          if (real) acc[e] += y[e] * x[e];
-          y[e] *= g[e];
-          dot += y[e] * x[e];
+        for (int d = kSeg / 2; d > 0; d >>= 1) {
+          ss += __shfl_xor_sync(0xffffffffu, ss, d);
+          t += __shfl_xor_sync(0xffffffffu, t, d);
         }
-        dot = seg_sum<kSeg>(dot) * inv_d;
+        const float q = rsqrtf(ss * p.inv_d + p.eps);
+        const float u = -(q * q * p.inv_d) * (q * t);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) y[e] = r * (y[e] - x[e] * dot);
+        for (int e = 0; e < 8; ++e) {
+          acc[e] = __ffma2_rn(y.x[e], __fmul2_rn(x.x[e], both(q)), acc[e]);
+          y.x[e] = __ffma2_rn(x.x[e], both(u), __fmul2_rn(wg.x[e], both(q)));
+        }
       }
-      if (w.on && h < H) {
-        uint4 a, bb;
-        pack16<DT>(y, a, bb);
-        if (!real) a = bb = make_uint4(0, 0, 0, 0);   // a padding token has no output
-        const long long at = b * dx.sb + l * dx.sl + h * dx.sh;
-        st16(dx.ptr, at + w.a, a);
-        st16(dx.ptr, at + w.b, bb);
-      }
+      pack16<DT>(y, a, bb);
+    }
+    if (w.on && cw.r * kRowsWarp + hl < H) {
+      st16(dst, a);
+      st16(dst + ab, bb);
+      dst += 2 * kRowsWarp * dx.sh;
     }
   }
   if (weight) {
-    float *mine = red[warp][lane / kSeg];
+    // the ring is idle now and takes the lanes' sums
+    copy_wait<0>();
+    __syncthreads();
+    float *red = reinterpret_cast<float *>(ring);   // [kWarps * kRowsWarp][kSeg * 16]
+    float *mine = red + (warp * kRowsWarp + hl) * (kSeg * 16);
     if (w.on) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        mine[w.a + e] = acc[e];
-        mine[w.b + e] = acc[8 + e];
+      for (int e = 0; e < 4; ++e) {
+        *reinterpret_cast<float2 *>(mine + w.a + 2 * e) = acc[e];
+        *reinterpret_cast<float2 *>(mine + w.b + 2 * e) = acc[4 + e];
       }
     }
     __syncthreads();
-    for (int d = threadIdx.x; d < p.D; d += kRopeBwdThreads) {
+    for (int d = threadIdx.x; d < p.D; d += kRopeThreads) {
       float sum = 0.0f;
-      for (int i = 0; i < kWarps; ++i)
-        for (int j = 0; j < kRowsWarp; ++j) sum += red[i][j][d];
+      for (int i = 0; i < kWarps * kRowsWarp; ++i) sum += red[i * (kSeg * 16) + d];
       p.part[static_cast<long long>(blockIdx.x) * p.D + d] = sum;
     }
   }
 }
 
-// dw[d] = the sum of the blocks' partials, in a fixed order: one block per
-// weight vector, 8 partial rows at a time.
+// dw[d] = the sum of the blocks' partials, in a fixed order: a block takes 32
+// columns of one weight, its 32 rows of threads every 32nd partial.
 __global__ void __launch_bounds__(1024) fa_rope_dw_kernel(const __grid_constant__ RopeParams p) {
-  __shared__ float red[8][128];
+  __shared__ float red[32][33];
   const bool is_q = blockIdx.x == 0;
   float *out = is_q ? p.dwq : p.dwk;
   if (!out) return;
-  const int d = threadIdx.x & 127, y = threadIdx.x >> 7;
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5, d = blockIdx.y * 32 + x;
   const float *part = p.part + (is_q ? 0 : static_cast<long long>(p.blocks_q) * p.D);
   const int n = is_q ? p.blocks_q : p.blocks_k;
   float sum = 0.0f;
   if (d < p.D)
-    for (int i = y; i < n; i += 8) sum += part[static_cast<long long>(i) * p.D + d];
-  red[y][d] = sum;
+#pragma unroll 8
+    for (int i = y; i < n; i += 32) sum += part[i * p.D + d];
+  red[y][x] = sum;
   __syncthreads();
-  if (y == 0 && d < p.D) {
-    for (int i = 1; i < 8; ++i) sum += red[i][d];
-    out[d] = sum;
-  }
+  sum = red[x][y];
+#pragma unroll
+  for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+  if (x == 0 && blockIdx.y * 32 + y < p.D) out[blockIdx.y * 32 + y] = sum;
 }
 
 }  // namespace fa
