@@ -907,7 +907,7 @@ def flash_fwd_paged(q, k_cache, v_cache, block_table, cu_q, kv_lens, scale=None,
 
     q: [total_q, H, D] fp16 or bf16, request b's new tokens in rows cu_q[b] ..
     cu_q[b + 1] (int32 [B + 1]); k_cache, v_cache: [pages, page_size, H_kv, D],
-    any strides, page_size 16, 32, 64 or a multiple of 128; block_table: int32
+    any strides, page_size a power of two, at least 16; block_table: int32
     [B, max_pages]; kv_lens: int32 [B], tokens in the cache with the new ones.
     Causal and window positions count to the end of the request.  ``scale``
     defaults to 1/sqrt(D).  The workspace is allocated here unless given (a

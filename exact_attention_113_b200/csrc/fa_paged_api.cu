@@ -2,6 +2,8 @@
 // checks, tensor maps, launches.  A translation unit of its own, with its own
 // device status word, which fa_get_device_status() also reads.
 #include <algorithm>
+#include <atomic>
+#include <chrono>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -73,15 +75,25 @@ bool encode(CUtensorMap *map, const void *base, int dtype, int rank, const long 
 }
 
 struct PagedWs {
-  size_t ml, rec, total;
+  size_t ml, ticket, total;
 };
 PagedWs paged_ws(int D, int grid) {
   const size_t rows = static_cast<size_t>(2) * grid * kPagedRows;
   PagedWs w;
   w.ml = rows * D * sizeof(float);
-  w.rec = w.ml + rows * sizeof(float2);
-  w.total = w.rec + static_cast<size_t>(grid) * sizeof(PagedRec);
+  w.ticket = w.ml + rows * sizeof(float2);
+  w.total = w.ticket + static_cast<size_t>(grid) * sizeof(unsigned long long);
   return w;
+}
+
+// A number for each call: 48 bits, not 0, from a start that differs between
+// processes, so that what a workspace held before does not pass for it.
+unsigned long long call_number() {
+  static std::atomic<unsigned long long> next{
+      static_cast<unsigned long long>(std::chrono::steady_clock::now().time_since_epoch().count()) *
+      0x9e3779b97f4a7c15ull};
+  const unsigned long long n = next.fetch_add(1) & 0xffffffffffffull;
+  return n ? n : next.fetch_add(1) & 0xffffffffffffull;
 }
 
 template <int D, int DT>
@@ -103,7 +115,6 @@ int launch_paged(const PagedParams &prm, int grid, cudaStream_t stream) {
     }
   }
   kern<<<grid, kThreads, smem, stream>>>(prm);
-  fa_paged_merge_kernel<D, DT><<<dim3(grid, kMergeY), kMergeThreads, 0, stream>>>(prm);
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -132,8 +143,7 @@ extern "C" int fa_fwd_paged(const void *q, long long q_stride_t, long long q_str
   if (total_q > kMaxLen || static_cast<long long>(B) * H_kv > kMaxLen) return FA_ERR_SHAPE;
   if (!head_dim_ok(D)) return FA_ERR_HEADDIM;
   if (dtype != FA_F16 && dtype != FA_BF16) return FA_ERR_DTYPE;
-  if (page_size < 16 || page_size > kMaxLen ||
-      (page_size < kBN ? kBN % page_size != 0 : page_size % kBN != 0))
+  if (page_size < 16 || page_size > kMaxLen || (page_size & (page_size - 1)) != 0)
     return FA_ERR_ARG;
   if (!std::isfinite(scale) || scale < 0.0f || table_stride < max_pages) return FA_ERR_ARG;
   if (total_q == 0) return FA_OK;
@@ -169,7 +179,7 @@ extern "C" int fa_fwd_paged(const void *q, long long q_stride_t, long long q_str
   p.total_q = total_q;
   p.tile_q = kBM / p.group;
   p.n_pages = num_pages;
-  p.page_size = page_size;
+  while ((1 << p.page_shift) < page_size) ++p.page_shift;
   p.max_kv = static_cast<int>(std::min<long long>(static_cast<long long>(max_pages) * page_size, kMaxLen));
   p.box_rows = std::min(page_size, kBN);
   // (a bound past the longest request is no bound)
@@ -180,7 +190,9 @@ extern "C" int fa_fwd_paged(const void *q, long long q_stride_t, long long q_str
   p.scale_log2 = sl2 < 1e-30f ? 1e-30f : sl2;
   p.ws_o = static_cast<float *>(workspace);
   p.ws_ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + ws.ml);
-  p.rec = reinterpret_cast<PagedRec *>(static_cast<char *>(workspace) + ws.rec);
+  p.ticket =
+      reinterpret_cast<unsigned long long *>(static_cast<char *>(workspace) + ws.ticket);
+  p.call = call_number();
   const int row_bytes = D * 2;
   const int cols = (row_bytes % 128 == 0 ? 128 : (row_bytes % 64 == 0 ? 64 : 32)) / 2;
   const long long qd[3] = {D, H, total_q}, qs[3] = {1, q_stride_h, q_stride_t};

@@ -16,10 +16,10 @@
 // equal pieces, one per CTA (one CTA per SM), so that one long request, many
 // short ones and causal triangles all fill the device.  A CTA walks its
 // piece, whole items and, at the ends, parts of two items; parts leave an
-// unnormalised fp32 O and (m, l) in the workspace and fa_paged_merge_kernel
-// joins them.  Each CTA finds its piece from the lengths by itself (a scan
-// over the requests during set-up), so a call needs no schedule from the
-// host, which does not know the lengths.
+// unnormalised fp32 O and (m, l) in the workspace, and the CTA that finishes an
+// item's last part joins them (nothing waits).  Each CTA finds its piece from
+// the lengths by itself (a scan over the requests during set-up), so a call
+// needs no schedule from the host, which does not know the lengths.
 //
 // A pair of two tiles runs as the forward kernel's ping-pong: per key block
 // S0, PV1(previous), S1, PV0, two softmax warpgroups in turns.  A single tile
@@ -27,9 +27,12 @@
 // to the other, each with its own (m, l, O), joined at the end; that keeps two
 // blocks in flight where one tile's S -> softmax -> PV chain would be exposed.
 //
-// Warps (384 threads): 0-3, 4-7 softmax; 8 MMA and TMEM; 9 K; 10 V; 11 Q.
-// TMEM: S0 [0,128), S1 [128,256) (P over the first 64 columns of each),
-// O0 [256,256+D), O1 [256+D,256+2D).
+// Warps (384 threads): 0-3, 4-7 softmax; 8 MMA and TMEM; 9 K; 10 V; 11 walks
+// the piece, announces each item to the others and loads its Q (a lone warp
+// takes over a microsecond for a step of the walk, so it runs ahead).
+// TMEM: S0 [0,128), S1 [128,256), O0 [256,256+D), O1 [256+D,256+2D); P_t over
+// the first 64 columns of S_t, or, for D <= 64, in [384+64t, 448+64t), so that
+// the next S_t is computed while the softmax works on this one.
 //
 // V rows no query of the item sees (behind the request's end, in a page's
 // unwritten tail, or before every window) are cleared in shared memory: their
@@ -40,16 +43,10 @@
 
 namespace fa {
 
-constexpr int kLoadWarpQ = 11;
-constexpr int kPagedMinUnits = 3;   // cost a CTA gets at least
-constexpr int kPagedRows = 2 * kBM; // rows of a work item
-
-struct PagedRec {   // what CTA c leaves for the merge (workspace)
-  int cont;         // its first item began in an earlier CTA
-  int ends;         // ... and ends here: this CTA's index names the merge
-  int b, h, pair;   // that item
-  int pad[3];
-};
+constexpr int kSchedWarp = 11;       // walks the work, loads Q
+constexpr int kPagedMinUnits = 3;    // cost a CTA gets at least
+constexpr int kPagedRows = 2 * kBM;  // rows of a work item
+constexpr int kItemRing = 3;         // items announced ahead
 
 struct PagedParams {
   CUtensorMap tm_q;   // (D, H, total_q), box (cols, G, TQ)
@@ -64,13 +61,14 @@ struct PagedParams {
   float *lse;                 // [total_q, H] or nullptr
   int B, H, H_kv, group, total_q;
   int tile_q;                 // tokens per tile
-  int n_pages, page_size, max_kv;   // max_kv: table columns * page size
+  int n_pages, page_shift, max_kv;  // page size 2^page_shift; max_kv: table columns * page size
   int box_rows;               // rows of one K/V copy: min(page size, 128)
   int wl, wr;                 // -1 = unbounded
   float scale_log2;
   float *ws_o;                // [2 * grid][kPagedRows][D]
   float2 *ws_ml;              // [2 * grid][kPagedRows]
-  PagedRec *rec;              // [grid]
+  unsigned long long *ticket; // [grid]
+  unsigned long long call;    // this call's number, 48 bits, not 0
 };
 
 // ------------------------------------------------------------------ the work line
@@ -140,88 +138,145 @@ __device__ __forceinline__ long long paged_head_cost(const PagedParams &p, const
   return sum;
 }
 
-// A place on the work line: request, K/V head, pair and the offset in its cost.
-struct PagedPos {
-  int b, h, pair, off;
-};
-
 // Set-up state in shared memory.
 struct PagedSetup {
   long long warp_sum[kThreads / 32];
-  long long u[2];       // first and last unit of this CTA's piece
-  PagedPos at[2];       // the same as places
-  int cost[2];          // the cost of the item at them
+  long long warp_rest[kThreads / 32];
+  long long rest[2];      // units of the piece's ends within their request
+  long long per_head[2];  // cost of one K/V head of that request
+  int b[2];               // that request (B: the end of the line)
 };
 
-// Finds this CTA's piece of the work line: st.u, st.at[0].  Called by all
-// threads of the block; ends with a barrier.
-__device__ __forceinline__ void paged_find_piece(const PagedParams &p, PagedSetup &st) {
+// a / b of non-negative numbers: in 32 bits where they fit (a quarter of the
+// instructions).
+__device__ __forceinline__ long long paged_div(long long a, long long b) {
+  if (((a | b) >> 32) == 0)
+    return static_cast<unsigned>(a) / static_cast<unsigned>(b);
+  return a / b;
+}
+
+// The work line cut in n pieces: piece c begins at cut(c).
+struct PagedCuts {
+  long long total, q;
+  int n, r;
+  __device__ __forceinline__ void set(long long total_, int ctas) {
+    total = total_;
+    n = static_cast<int>(max(1ll, min(static_cast<long long>(ctas), total / kPagedMinUnits)));
+    q = paged_div(total, n);
+    r = static_cast<int>(total - q * n);
+  }
+  __device__ __forceinline__ long long at(int c) const {
+    return c >= n ? total : q * c + static_cast<unsigned>(r * c) / static_cast<unsigned>(n);
+  }
+  // the last piece that begins at or before u
+  __device__ __forceinline__ int last(long long u) const {
+    int c = static_cast<int>(min(static_cast<long long>(n - 1), paged_div(u * n, total)));
+    while (c > 0 && at(c) > u) --c;
+    while (c + 1 < n && at(c + 1) <= u) ++c;
+    return c;
+  }
+};
+
+// All threads: the line's length and the requests that the ends of this CTA's
+// piece lie in.  Ends with a barrier.
+__device__ __forceinline__ void paged_find_piece(const PagedParams &p, PagedSetup &st,
+                                                 PagedCuts &cuts) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int kWarps = kThreads / 32;
   auto cost_of = [&](int b) {
     PagedReq r;
     r.q_start = r.q_len = r.kv_len = 0;
     if (b < p.B) r = paged_req(p, b);
-    return paged_head_cost(p, r) * p.H_kv;
+    return paged_head_cost(p, r);
   };
-  const long long first = cost_of(tid);
-  long long mine = first;
-  for (int base = kThreads; base < p.B; base += kThreads) mine += cost_of(base + tid);
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, d);
-  if (lane == 0) st.warp_sum[warp] = mine;
-  __syncthreads();
-  long long total = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) total += st.warp_sum[w];
-  // pieces: as many as there are CTAs, none below kPagedMinUnits
-  const long long n = max(1ll, min(static_cast<long long>(gridDim.x), total / kPagedMinUnits));
-  const long long c = blockIdx.x;
-  const long long want[2] = {c >= n ? total : total / n * c + total % n * c / n,
-                             c + 1 >= n ? total : total / n * (c + 1) + total % n * (c + 1) / n};
-  if (tid < 2) {
-    st.at[tid] = {p.B, 0, 0, 0};
-    st.u[tid] = want[tid];
-    st.cost[tid] = 0;
-  }
-  long long before = 0;
-  for (int base = 0; base < p.B; base += kThreads) {
-    __syncthreads();
-    const long long s = base == 0 ? first : cost_of(base + tid);
-    long long incl = s;
+  auto scan = [&](long long v) {
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, incl, d);
-      if (lane >= d) incl += v;
+      const long long o = __shfl_up_sync(0xffffffffu, v, d);
+      if (lane >= d) v += o;
     }
+    return v;
+  };
+  if (tid < 2) st.b[tid] = p.B;
+  long long head = cost_of(tid), s = head * p.H_kv, incl = scan(s), rest = 0;
+  for (int base = kThreads; base < p.B; base += kThreads) rest += cost_of(base + tid) * p.H_kv;
+  if (p.B > kThreads) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, d);
+  }
+  if (lane == 31) {
+    st.warp_sum[warp] = incl;
+    st.warp_rest[warp] = rest;
+  }
+  __syncthreads();
+  long long total = 0, pre = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) pre += st.warp_sum[w];
+    total += st.warp_sum[w];
+  }
+  long long before = total;   // of the requests so far
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) total += st.warp_rest[w];
+  cuts.set(total, gridDim.x);
+  const int c = blockIdx.x;
+  const long long want[2] = {cuts.at(c), cuts.at(c + 1)};
+  auto look = [&](int b, long long lo) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      if (s > 0 && want[e] >= lo && want[e] < lo + s) {
+        st.b[e] = b;
+        st.rest[e] = want[e] - lo;
+        st.per_head[e] = head;
+      }
+  };
+  look(tid, pre + incl - s);
+  for (int base = kThreads; base < p.B; base += kThreads) {
+    head = cost_of(base + tid);
+    s = head * p.H_kv;
+    incl = scan(s);
+    __syncthreads();
     if (lane == 31) st.warp_sum[warp] = incl;
     __syncthreads();
-    long long pre = before;
+    pre = before;
+#pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       if (w < warp) pre += st.warp_sum[w];
       before += st.warp_sum[w];
     }
-    const long long lo = pre + incl - s;
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-      if (s > 0 && want[e] >= lo && want[e] < lo + s) {
-        st.at[e].b = base + tid;
-        st.u[e] = want[e] - lo;   // rest within the request, for the next step
-      }
+    look(base + tid, pre + incl - s);
   }
-  __syncthreads();
-  // head, pair and offset: warp e searches for end e
-  if (warp < 2 && st.at[warp].b < p.B) {
-    const int e = warp;
-    const PagedReq r = paged_req(p, st.at[e].b);
+}
+
+// One part of an item, as the roles see it.
+struct PagedItem {
+  int h, tok0, nt0, nt1;     // K/V head (-1: no more items); first tile's first packed row; tokens
+  int first, kv_len, lo, hi; // position of the first token; key blocks of the part
+  int lo0, hi0, lo1, hi1;    // ... of each tile
+  int klo, khi, slot, b;     // keys some token of the item sees; -1: the whole item, else the part's slot
+  int cta0, parts, pad[2];   // a cut item: the CTA where it began, its parts
+};
+
+// Walks a CTA's piece (one warp).
+struct PagedWalk {
+  int b, h, pair, off;
+  long long u, end;          // on the work line: here, and the piece's end
+  PagedReq r;
+
+  // The place and cost of the item at end e of the piece; u moved to the border
+  // where a cut one unit behind an item's start would leave a part without a
+  // key block, and where it would leave the next part only the last one.
+  __device__ __forceinline__ void locate(const PagedParams &p, const PagedSetup &st, int e,
+                                         long long &at) {
+    const int lane = threadIdx.x & 31;
+    b = st.b[e];
+    h = pair = off = 0;
+    if (b >= p.B) return;
+    r = paged_req(p, b);
     const int np = paged_pairs(p, r.q_len);
-    PagedReq alone = r;
-    if (lane != 0) alone.q_len = 0;
-    const long long per_head = __shfl_sync(0xffffffffu, paged_head_cost(p, alone), 0);
-    const long long rest = st.u[e];
-    const int h = static_cast<int>(rest / per_head);
-    long long in = rest - h * per_head;
-    int pair = 0, off = 0, cost = 0;
+    h = static_cast<int>(paged_div(st.rest[e], st.per_head[e]));
+    long long in = st.rest[e] - h * st.per_head[e];
+    int cost = 0;
     for (int base = 0; base < np; base += 32) {
       const int i = base + lane;
       const int cst = i < np ? paged_blocks(p, r, i) + 1 : 0;
@@ -241,56 +296,20 @@ __device__ __forceinline__ void paged_find_piece(const PagedParams &p, PagedSetu
       }
       in -= __shfl_sync(0xffffffffu, incl, 31);
     }
-    // A cut one unit behind an item's start would leave a part without a key
-    // block, one unit before its end a part of one: move both to the border.
-    long long u = want[e];
     if (off == 1) {
       off = 0;
-      u -= 1;
+      at -= 1;
     } else if (off == cost - 1 && off > 0) {
-      off = cost;
-      u += 1;
-    }
-    if (lane == 0) {
-      st.at[e].h = h;
-      st.at[e].pair = pair;
-      st.at[e].off = off;
-      st.u[e] = u;
-      st.cost[e] = cost;
+      at += 1;
+      advance(p);
     }
   }
-  __syncthreads();
-}
-
-// One part of an item, as a CTA's roles see it (warp-uniform).
-struct PagedPart {
-  int b, h, pair;
-  int tok0;            // packed row of the first tile's first token
-  int nt0, nt1;        // tokens of the tiles
-  int first;           // position of the first token
-  int kv_len;
-  int lo, hi;          // key blocks of the part (both tiles)
-  int lo0, hi0, lo1, hi1;   // ... of each tile
-  int klo, khi;        // keys some token of the item sees
-  int slot;            // -1: the whole item; 0 / 1: workspace slot of the part
-};
-
-// Walks a CTA's piece.  Every role walks it by itself.
-struct PagedWalk {
-  int b, h, pair, off;
-  long long left;
-  PagedReq r;
-
-  __device__ __forceinline__ void start(const PagedParams &p, const PagedSetup &st) {
-    b = st.at[0].b;
-    h = st.at[0].h;
-    pair = st.at[0].pair;
-    off = st.at[0].off;
-    left = st.u[1] - st.u[0];
-    if (b < p.B) {
-      r = paged_req(p, b);
-      if (off >= st.cost[0]) advance(p);   // the cut moved to the item's end
-    }
+  __device__ __forceinline__ void start(const PagedParams &p, const PagedSetup &st,
+                                        const PagedCuts &cuts) {
+    end = cuts.at(blockIdx.x + 1);
+    locate(p, st, 1, end);
+    u = cuts.at(blockIdx.x);
+    locate(p, st, 0, u);
   }
   __device__ __forceinline__ void advance(const PagedParams &p) {
     off = 0;
@@ -303,11 +322,13 @@ struct PagedWalk {
       if (r.q_len > 0) return;
     }
   }
-  __device__ __forceinline__ bool next(const PagedParams &p, PagedPart &t) {
-    if (left <= 0 || b >= p.B) return false;
+  __device__ __forceinline__ bool next(const PagedParams &p, const PagedCuts &cuts, PagedItem &t) {
+    if (u >= end || b >= p.B) {
+      t.h = -1;
+      return false;
+    }
     t.b = b;
     t.h = h;
-    t.pair = pair;
     const int i0 = pair * 2 * p.tile_q;
     t.tok0 = r.q_start + i0;
     t.nt0 = min(p.tile_q, r.q_len - i0);
@@ -321,19 +342,26 @@ struct PagedWalk {
     const int blocks = t.khi < t.klo ? 0 : t.khi / kBN - t.klo / kBN + 1;
     const int lo = t.klo / kBN;
     const int cost = blocks + 1;
-    const int end = static_cast<int>(min(static_cast<long long>(cost), off + left));
+    const int to = static_cast<int>(min(static_cast<long long>(cost), off + (end - u)));
     t.lo = lo + max(off - 1, 0);
-    t.hi = end >= cost ? lo + blocks : lo + end - 1;
-    t.slot = off > 0 ? 0 : (end < cost ? 1 : -1);
+    t.hi = to >= cost ? lo + blocks : lo + to - 1;
+    t.slot = off > 0 ? 0 : (to < cost ? 1 : -1);
     t.lo0 = max(t.lo, klo0 / kBN);
     t.hi0 = khi0 < klo0 ? t.lo0 : max(t.lo0, min(t.hi, khi0 / kBN + 1));
     t.lo1 = max(t.lo, klo1 / kBN);
     t.hi1 = khi1 < klo1 ? t.lo1 : max(t.lo1, min(t.hi, khi1 / kBN + 1));
-    left -= end - off;
-    if (end >= cost)
+    t.cta0 = t.parts = 0;
+    if (t.slot >= 0) {
+      // the first and the last piece with a part of the item, by the cuts
+      // before they move to the borders (see locate)
+      t.cta0 = cuts.last(u - off + 1);
+      t.parts = cuts.last(u - off + cost - 2) - t.cta0 + 1;
+    }
+    u += to - off;
+    if (to >= cost)
       advance(p);
     else
-      off = end;
+      off = to;
     return true;
   }
 };
@@ -341,33 +369,42 @@ struct PagedWalk {
 // ------------------------------------------------------------------ shared memory
 template <int kSlots>
 struct PagedBars {
+  uint64_t item_full[kItemRing];
+  uint64_t item_empty[kItemRing];
   uint64_t q_full[2];    // Q slot filled
   uint64_t q_empty[2];   // every S that reads it is done
   uint64_t full[kSlots];
   uint64_t empty[kSlots];
   uint64_t v_ragged;     // the copy of a V block whose hidden rows are cleared
   uint64_t s_full[2];
+  uint64_t s_free[2];    // the softmax holds S_t in registers (D <= 64)
   uint64_t p_full[2];
   uint64_t pv_done[2];
   uint64_t o_free[2];    // O_t has been read by the epilogue
-  uint64_t ml_full;      // single tile: warpgroup 1's (m, l) written
-  uint64_t ml_free;      // ... and read
+  uint64_t ml_full[2];   // single tile: warpgroup's (m, l) written
+  uint64_t ml_free[2];   // ... and read
+  uint64_t part_done;    // a part's rows are in the workspace
+  uint64_t part_last;    // whether they were the item's last is known
   uint64_t mma_done;
   uint32_t tmem_base;
   int abort_flag;
+  int is_last;
+  int ticketed[2];       // the CTA's parts whose arrival has been counted
+  PagedItem item[kItemRing];
   PagedSetup setup;
 };
 
 template <int D>
 struct PagedGeo : Geo<D, 2> {
   using G = Geo<D, 2>;
-  static constexpr int kOffXch = G::kOffBar + 1024;       // (m, l) of 128 rows
-  static constexpr int kUsedPaged = kOffXch + kBM * 8;
-  // (one CTA per SM, as the forward: at least 118 KB)
-  static constexpr int kSmemPaged =
-      (kUsedPaged + 1024 > 118 * 1024) ? kUsedPaged + 1024 : 118 * 1024;
+  static constexpr int kBarBytesPaged = 1024;
+  static constexpr int kOffXch = G::kOffBar + kBarBytesPaged;   // (m, l) of 128 rows, twice
+  static constexpr int kUsedPaged = kOffXch + 2 * kBM * 8;
+  // (one CTA per SM, as the forward: at least 118 KB.  The base is 1024-byte
+  // aligned by its declaration, as there is no other shared memory.)
+  static constexpr int kSmemPaged = kUsedPaged > 118 * 1024 ? kUsedPaged : 118 * 1024;
   static_assert(kSmemPaged <= 232448, "shared memory budget");
-  static_assert(sizeof(PagedBars<G::kSlots>) <= 1024, "barrier block");
+  static_assert(sizeof(PagedBars<G::kSlots>) <= kBarBytesPaged, "barrier block");
 };
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, uint32_t bar,
@@ -392,6 +429,108 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
+}
+
+// Counts a part's arrival; true for the item's last.  The word holds the
+// call's number and the parts so far; with another number in it (a new
+// workspace, whatever it held) the count is 0, and the last arrival leaves 0.
+__device__ __forceinline__ bool paged_ticket(const PagedParams &p, int cta0, int parts) {
+  unsigned long long *at = p.ticket + cta0;
+  unsigned long long old = *reinterpret_cast<volatile unsigned long long *>(at);
+  while (true) {
+    const unsigned long long n = ((old >> 16) == p.call ? (old & 0xffffull) : 0ull) + 1;
+    const bool last = n == static_cast<unsigned long long>(parts);
+    const unsigned long long now = atomicCAS(at, old, last ? 0ull : (p.call << 16) | n);
+    if (now == old) return last;
+    old = now;
+  }
+}
+
+// Joins the parts of a cut item: m = max_i m_i, w_i = 2^(m_i - m),
+// O = sum_i w_i O_i / sum_i w_i l_i, lse = (m + log2 l) ln 2, in the order of
+// the parts, so that the result does not depend on which came last.  Part i
+// lies in slot 1 of CTA cta0 (i = 0) or slot 0 of CTA cta0 + i.  A warp joins
+// kRows rows at a time, lane / kRows takes a part's (m, l), and the rows' parts
+// are loaded together: the time is that of the loads' latency.
+template <int D, int DT>
+__device__ __forceinline__ void paged_merge(const PagedParams &p, const PagedItem &t, int warp,
+                                            int warps) {
+  constexpr int kRows = 8, kLanes = 32 / kRows;
+  const int lane = threadIdx.x & 31;
+  const int rows0 = t.nt0 * p.group, rows = rows0 + max(t.nt1, 0) * p.group;
+  auto place = [&](int k) {   // row k of the item in a slot
+    return static_cast<size_t>(k >= rows0 ? kBM + k - rows0 : k);
+  };
+  auto slot_of = [&](int i) {
+    return static_cast<size_t>(2 * (t.cta0 + i) + (i == 0 ? 1 : 0)) * kPagedRows;
+  };
+  for (int k0 = warp * kRows; k0 < rows; k0 += warps * kRows) {
+    // (rows behind the last one repeat it: their lanes only load)
+    const int mine = min(k0 + lane / kLanes, rows - 1);
+    float m = -INFINITY;
+    for (int i = lane % kLanes; i < t.parts; i += kLanes)
+      m = fmaxf(m, __ldcg(&p.ws_ml[slot_of(i) + place(mine)]).x);
+#pragma unroll
+    for (int d = kLanes / 2; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    const float m_sub = m == -INFINITY ? 0.0f : m;
+    float4 acc[kRows];
+#pragma unroll
+    for (int e = 0; e < kRows; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.0f;
+    for (int i0 = 0; i0 < t.parts; i0 += kLanes) {
+      // the weights of the next kLanes parts of the lane's row
+      const int i = i0 + lane % kLanes;
+      float w = 0.0f, wl = 0.0f;
+      if (i < t.parts) {
+        const float2 ml = __ldcg(&p.ws_ml[slot_of(i) + place(mine)]);
+        w = ex2(ml.x - m_sub);     // a part without a visible key: 0
+        wl = w * ml.y;
+      }
+#pragma unroll 2
+      for (int j = 0; j < kLanes && i0 + j < t.parts; ++j) {
+        l += __shfl_sync(0xffffffffu, wl, (lane & ~(kLanes - 1)) + j);
+        float4 o[kRows];
+#pragma unroll
+        for (int e = 0; e < kRows; ++e)
+          if (lane * 4 < D)
+            o[e] = __ldcg(reinterpret_cast<const float4 *>(
+                              p.ws_o + (slot_of(i0 + j) + place(min(k0 + e, rows - 1))) * D) + lane);
+#pragma unroll
+        for (int e = 0; e < kRows; ++e) {
+          const float we = __shfl_sync(0xffffffffu, w, e * kLanes + j);
+          acc[e].x += we * o[e].x;
+          acc[e].y += we * o[e].y;
+          acc[e].z += we * o[e].z;
+          acc[e].w += we * o[e].w;
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < kRows; ++e) {
+      const int k = k0 + e;
+      const float le = __shfl_sync(0xffffffffu, l, e * kLanes);
+      const float me = __shfl_sync(0xffffffffu, m, e * kLanes);
+      if (k < rows) {
+        const int tile = k >= rows0 ? 1 : 0, rr = k - tile * rows0;
+        const float inv = le > 0.0f ? 1.0f / le : 0.0f;
+        const int tok = t.tok0 + tile * p.tile_q + rr / p.group;
+        const int head = t.h * p.group + rr % p.group;
+        if (lane * 4 < D)
+          *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.out) +
+                                     2 * (static_cast<long long>(tok) * p.out_st +
+                                          static_cast<long long>(head) * p.out_sh + 4 * lane)) =
+              make_uint2(pack2<DT>(acc[e].x * inv, acc[e].y * inv),
+                         pack2<DT>(acc[e].z * inv, acc[e].w * inv));
+        if (lane == 0 && p.lse != nullptr)
+          p.lse[static_cast<size_t>(tok) * p.H + head] =
+              le > 0.0f ? (me + __log2f(le)) * 0.6931471805599453f : -INFINITY;
+      }
+    }
+  }
+}
+
 // ------------------------------------------------------------------ the kernel
 template <int D, int DT>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -400,9 +539,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   using PG = PagedGeo<D>;
   constexpr int kSlots = G::kSlots;
   constexpr int kKStep = 16;
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t *smem = reinterpret_cast<uint8_t *>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  constexpr bool kSplitP = G::kSplitP;   // P in columns of its own (D <= 64)
+  extern __shared__ __align__(1024) uint8_t smem[];
   PagedBars<kSlots> *bars = reinterpret_cast<PagedBars<kSlots> *>(smem + G::kOffBar);
   volatile int *abort_flag = &bars->abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -410,31 +548,41 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sRing = smem_u32(smem + G::kOffRing);
 
   // ---- setup
-  if (tid == 0) {
+  if (sQ & 1023u) {   // (never: see PagedGeo)
+    if (tid == 0) atomicOr(&g_fa_status, 1u);
+    return;
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(&bars->tmem_base), kTmemCols);
+    tmem_relinquish();
+  }
+  if (tid == kLoadWarp * 32) {
     for (int t = 0; t < 2; ++t) {
       mbar_init(smem_u32(&bars->q_full[t]), 1);
       mbar_init(smem_u32(&bars->q_empty[t]), 1);
       mbar_init(smem_u32(&bars->s_full[t]), 1);
-      mbar_init(smem_u32(&bars->p_full[t]), kBM);
+      mbar_init(smem_u32(&bars->s_free[t]), 4);
+      mbar_init(smem_u32(&bars->p_full[t]), 4);
       mbar_init(smem_u32(&bars->pv_done[t]), 1);
-      mbar_init(smem_u32(&bars->o_free[t]), kBM);
+      mbar_init(smem_u32(&bars->o_free[t]), 8);
+      mbar_init(smem_u32(&bars->ml_full[t]), 4);
+      mbar_init(smem_u32(&bars->ml_free[t]), 4);
+    }
+    for (int s = 0; s < kItemRing; ++s) {
+      mbar_init(smem_u32(&bars->item_full[s]), 1);
+      mbar_init(smem_u32(&bars->item_empty[s]), 11);   // MMA, K, V, eight softmax warps
     }
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(smem_u32(&bars->full[s]), 1);
       mbar_init(smem_u32(&bars->empty[s]), 1);
     }
     mbar_init(smem_u32(&bars->v_ragged), 1);
-    mbar_init(smem_u32(&bars->ml_full), kBM);
-    mbar_init(smem_u32(&bars->ml_free), kBM);
+    mbar_init(smem_u32(&bars->part_done), 8);
+    mbar_init(smem_u32(&bars->part_last), 1);
     mbar_init(smem_u32(&bars->mma_done), 1);
     bars->abort_flag = 0;
+    bars->ticketed[0] = bars->ticketed[1] = 0;
     fence_mbar_init();
-  }
-  if (warp == kMmaWarp) {
-    tmem_alloc(smem_u32(&bars->tmem_base), kTmemCols);
-    tmem_relinquish();
-  }
-  if (tid == kLoadWarpQ * 32) {
     prefetch_tensormap(&p.tm_q);
     prefetch_tensormap(&p.tm_k);
     prefetch_tensormap(&p.tm_v);
@@ -447,37 +595,52 @@ __global__ void __launch_bounds__(kThreads, 1)
       reinterpret_cast<uint4 *>(smem + G::kOffQ)[i] = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
   }
-  paged_find_piece(p, bars->setup);
+  PagedCuts cuts;
+  paged_find_piece(p, bars->setup, cuts);
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = bars->tmem_base;
-  PagedWalk walk;
-  walk.start(p, bars->setup);
-  if (tid == 0) {
-    PagedRec rec = {};
-    PagedWalk w = walk;
-    PagedPart part;
-    if (w.next(p, part) && part.slot == 0) {
-      rec.cont = 1;
-      rec.ends = w.off == 0;
-      rec.b = part.b;
-      rec.h = part.h;
-      rec.pair = part.pair;
-    }
-    p.rec[blockIdx.x] = rec;
-  }
+
+  // Takes item k from the ring; the warp's fields are in registers when it
+  // returns.  False: no more, or given up.
+  bool ok = true;
+  auto take = [&](int k, PagedItem &t) -> bool {
+    const int s = k % kItemRing;
+    ok = mbar_wait_warp(smem_u32(&bars->item_full[s]), (k / kItemRing) & 1, abort_flag);
+    if (!ok) return false;
+    t = bars->item[s];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&bars->item_empty[s]));
+    return t.h >= 0;
+  };
 
   if (warp >= 8) {
   regs_dec<RegSplit::kSmall>();
-  if (warp == kLoadWarpQ) {
-    // =================================================== Q producer
-    // A tile with key blocks takes the next of the two Q slots.
-    PagedPart t;
-    int nq = 0;
-    bool ok = true;
+  if (warp == kSchedWarp) {
+    // =================================================== schedule and Q
+    // Items are announced up to kItemRing ahead of their last reader, one
+    // ahead of their Q: a tile with key blocks takes the next of two Q slots.
+    PagedWalk walk;
+    walk.start(p, bars->setup, cuts);
+    PagedItem t, ahead;
+    int nq = 0, k = 0;
     const uint64_t pol = policy_evict_first();
-    auto load = [&](int tok) {
+    auto announce = [&](PagedItem &it) -> bool {
+      const bool more = walk.next(p, cuts, it);
+      const int s = k % kItemRing;
+      if (k >= kItemRing)
+        ok = mbar_wait_warp(smem_u32(&bars->item_empty[s]), (k / kItemRing - 1) & 1, abort_flag);
+      if (!ok) return false;
+      if (lane == 0) {
+        bars->item[s] = it;
+        mbar_arrive(smem_u32(&bars->item_full[s]));
+      }
+      __syncwarp();
+      ++k;
+      return more;
+    };
+    auto load = [&](int h, int tok) {
       const int s = nq & 1;
       if (nq >= 2) ok = mbar_wait_warp(smem_u32(&bars->q_empty[s]), ((nq >> 1) - 1) & 1, abort_flag);
       if (!ok) return;
@@ -487,18 +650,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int bx = 0; bx < G::kNumBox; ++bx)
           tma_load_3d(sQ + s * G::kTileBytes + bx * G::kBoxBytes, &p.tm_q, bar, bx * G::kBoxCols,
-                      t.h * p.group, tok, pol);
+                      h * p.group, tok, pol);
       }
       __syncwarp();
       ++nq;
     };
-    while (ok && walk.next(p, t)) {
-      if (t.hi0 > t.lo0) load(t.tok0);
-      if (ok && t.hi1 > t.lo1) load(t.tok0 + p.tile_q);
+    bool more = announce(t);
+    while (ok && more) {
+      more = announce(ahead);
+      if (ok && t.hi0 > t.lo0) load(t.h, t.tok0);
+      if (ok && t.hi1 > t.lo1) load(t.h, t.tok0 + p.tile_q);
+      t = ahead;
     }
     if (!ok)   // let the copies in flight land before the CTA exits
-      for (int k = max(0, nq - 2); k < nq; ++k)
-        mbar_wait_slow(smem_u32(&bars->q_full[k & 1]), (k >> 1) & 1, abort_flag, false);
+      for (int n = max(0, nq - 2); n < nq; ++n)
+        mbar_wait_slow(smem_u32(&bars->q_full[n & 1]), (n >> 1) & 1, abort_flag, false);
   } else if (warp == kLoadWarp || warp == kLoadWarpV) {
     // =================================================== K and V producers
     // Lane i copies the i-th run of box_rows rows of a key block (one page, or
@@ -510,21 +676,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int base = is_k ? 0 : G::kSlotsK;
     const CUtensorMap *map = is_k ? &p.tm_k : &p.tm_v;
     const int per_block = kBN / p.box_rows;          // copies of rows per block
+    const int in_mask = (1 << p.page_shift) - 1;
     const uint64_t pol = policy_evict_last();
-    PagedPart t;
+    PagedItem t;
     int q = 0;             // fills so far
     int ragged = 0;        // V: ragged blocks so far
     int pend_slot = -1, pend_lo = 0, pend_hi = 0;   // V: the one not yet cleared
-    bool ok = true;
 
     // rows [0, lo) and [hi, 128) of the ragged block := 0, then release it
     auto clear = [&]() {
       uint8_t *tile = smem + G::kOffRing + pend_slot * G::kTileBytes;
       constexpr int kUnits = G::kUnitsPerBoxRow;
-#pragma unroll
+#pragma unroll 1
       for (int bx = 0; bx < G::kNumBox; ++bx) {
         uint4 *box = reinterpret_cast<uint4 *>(tile + bx * G::kBoxBytes);
+#pragma unroll 1
         for (int i = lane; i < pend_lo * kUnits; i += 32) box[i] = make_uint4(0, 0, 0, 0);
+#pragma unroll 4
         for (int i = pend_hi * kUnits + lane; i < kBN * kUnits; i += 32)
           box[i] = make_uint4(0, 0, 0, 0);
       }
@@ -538,16 +706,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = mbar_wait_warp(smem_u32(&bars->v_ragged), (ragged - 1) & 1, abort_flag);
       if (ok) clear();
     };
-    // Wait for a free slot; a ragged block that lands meanwhile is released
-    // (the slot may be freed only by what waits for it).
-    auto wait_slot = [&](uint32_t bar, uint32_t parity) {
+    // Wait for a barrier; a ragged block that lands meanwhile is released (the
+    // barrier may be one that only what waits for the block completes).
+    auto wait_clearing = [&](uint32_t bar, uint32_t parity) {
       const unsigned long long t0 = pend_slot >= 0 ? globaltimer_ns() : 0;
       while (pend_slot >= 0) {
-        if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return;
         if (__all_sync(0xffffffffu, mbar_test(smem_u32(&bars->v_ragged), (ragged - 1) & 1))) {
           clear();
           break;
         }
+        if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return;
         const bool late = globaltimer_ns() - t0 > kWaitLimitNs;
         if (__any_sync(0xffffffffu, late)) {
           *abort_flag = 1;
@@ -561,20 +729,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = mbar_wait_warp(bar, parity, abort_flag);
     };
 
-    while (ok && walk.next(p, t)) {
+    for (int k = 0; ok; ++k) {
+      if (pend_slot >= 0)
+        wait_clearing(smem_u32(&bars->item_full[k % kItemRing]), (k / kItemRing) & 1);
+      if (!ok || !take(k, t)) break;
       const int *row = p.table + t.b * p.table_stride;
       // page of this lane's rows of block j (-1: none), read one block ahead
       auto page_of = [&](int j) {
         const int pos = j * kBN + lane * p.box_rows;
         if (lane >= per_block || j >= t.hi || pos > t.khi || pos + p.box_rows <= t.klo) return -1;
-        return __ldg(row + pos / p.page_size);
+        return __ldg(row + (pos >> p.page_shift));
       };
       int page = page_of(t.lo);
       for (int j = t.lo; j < t.hi; ++j, ++q) {
         const int next_page = page_of(j + 1);
         const int slot = base + q % nslot;
         if (q >= nslot) {
-          wait_slot(smem_u32(&bars->empty[slot]), ((q / nslot) - 1) & 1);
+          wait_clearing(smem_u32(&bars->empty[slot]), ((q / nslot) - 1) & 1);
           if (!ok) break;
         }
         const int k0 = j * kBN;
@@ -587,7 +758,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive_expect_tx(bar, G::kTileBytes);
         __syncwarp();
         if (lane < per_block) {
-          const int in_page = (k0 + lane * p.box_rows) % p.page_size;
+          const int in_page = (k0 + lane * p.box_rows) & in_mask;
           if (page < 0 || page >= p.n_pages) page = p.n_pages;
           const uint32_t dst = sRing + slot * G::kTileBytes + lane * p.box_rows * G::kSwBytes;
 #pragma unroll
@@ -611,9 +782,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // copy lands on v_ragged
       if (pend_slot >= 0)
         mbar_wait_slow(smem_u32(&bars->v_ragged), (ragged - 1) & 1, abort_flag, false);
-      for (int k = max(0, q - nslot); k < q; ++k)
-        if (base + k % nslot != pend_slot)
-          mbar_wait_slow(smem_u32(&bars->full[base + k % nslot]), (k / nslot) & 1, abort_flag,
+      for (int n = max(0, q - nslot); n < q; ++n)
+        if (base + n % nslot != pend_slot)
+          mbar_wait_slow(smem_u32(&bars->full[base + n % nslot]), (n / nslot) & 1, abort_flag,
                          false);
     }
   } else {
@@ -621,10 +792,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t kIdescS = make_idesc_f16(kBM, kBN, DT, 0, 0);
     constexpr uint32_t kIdescPV = make_idesc_f16(kBM, D, DT, 0, 1);
     constexpr uint32_t kHi = desc_hi(8 * G::kSwBytes, G::kLayout);
-    PagedPart t;
-    bool ok = true;
+    PagedItem t;
     int nq = 0;                   // Q slots used so far
     int q = 0;                    // key blocks so far (K and V fills)
+    int ns0 = 0, ns1 = 0;         // S tiles issued so far
     int np0 = 0, np1 = 0;         // P tiles taken so far
     int no0 = 0, no1 = 0;         // O tiles begun so far
     auto kslot = [&](int n) { return n % G::kSlotsK; };
@@ -636,7 +807,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (elect_one()) tc_commit(smem_u32(bar));
       __syncwarp();
     };
+    // S_u = Q K^T; with P beside S it waits until the softmax holds the last
+    // S_u, otherwise the PV before it (which reads P over S) was issued first
     auto issue_s = [&](int u, int qs, int slot) {
+      const int n = u ? ns1 : ns0;
+      if (kSplitP && n > 0) wait(&bars->s_free[u], n - 1);
+      if (!ok) return;
+      tc_fence_after_sync();
       const uint32_t qlo = desc_lo(sQ + qs * G::kTileBytes, 16);
       const uint32_t klo = desc_lo(sRing + slot * G::kTileBytes, 16);
       const uint32_t d_tmem = tmem + (u ? 128u : 0u);
@@ -651,6 +828,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_commit(smem_u32(&bars->s_full[u]));
       }
       __syncwarp();
+      if (u) ++ns1; else ++ns0;
     };
     // O_u (+)= P_u V; the item's first product of a tile waits until the
     // epilogue has read the last item's O
@@ -660,7 +838,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) return;
       tc_fence_after_sync();
       const uint32_t vlo = desc_lo(sRing + slot * G::kTileBytes, G::kBoxBytes);
-      const uint32_t a_tmem = tmem + (u ? 128u : 0u);
+      const uint32_t a_tmem = tmem + (kSplitP ? 384u + (u ? 64u : 0u) : (u ? 128u : 0u));
       const uint32_t d_tmem = tmem + 256u + (u ? D : 0u);
       if (elect_one()) {
 #pragma unroll
@@ -674,7 +852,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (first) { if (u) ++no1; else ++no0; }
     };
 
-    while (ok && walk.next(p, t)) {
+    for (int k = 0; ok && take(k, t); ++k) {
       if (t.hi <= t.lo) continue;
       const int q0 = q;                       // fill index of block lo
       if (t.nt1 <= 0) {
@@ -685,21 +863,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int nb = t.hi - t.lo;
         auto step_s = [&](int n) {
           wait(&bars->full[kslot(q0 + n)], (q0 + n) / G::kSlotsK);
+          if (ok) issue_s(n & 1, qs, kslot(q0 + n));
           if (!ok) return;
-          tc_fence_after_sync();
-          issue_s(n & 1, qs, kslot(q0 + n));
           commit(&bars->empty[kslot(q0 + n)]);
           if (n == nb - 1) commit(&bars->q_empty[qs]);
         };
-        if (ok) step_s(0);
-        if (ok && nb > 1) step_s(1);
-        for (int n = 0; n < nb && ok; ++n) {
+        auto step_pv = [&](int n) {
           wait(&bars->full[vslot(q0 + n)], (q0 + n) / G::kSlotsV);
-          if (!ok) break;
-          issue_pv(n & 1, vslot(q0 + n), n < 2);
-          if (!ok) break;
-          commit(&bars->empty[vslot(q0 + n)]);
-          if (n + 2 < nb) step_s(n + 2);
+          if (ok) issue_pv(n & 1, vslot(q0 + n), n < 2);
+          if (ok) commit(&bars->empty[vslot(q0 + n)]);
+        };
+        for (int n = 0; n < nb + 2 && ok; ++n) {
+          if (kSplitP) {
+            if (n < nb) step_s(n);
+            if (ok && n >= 2) step_pv(n - 2);
+          } else {
+            if (n >= 2) step_pv(n - 2);
+            if (ok && n < nb) step_s(n);
+          }
         }
       } else {
         const bool act0 = t.hi0 > t.lo0, act1 = t.hi1 > t.lo1;
@@ -715,32 +896,56 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         auto in0 = [&](int j) { return j >= t.lo0 && j < t.hi0; };
         auto in1 = [&](int j) { return j >= t.lo1 && j < t.hi1; };
-        wait(&bars->full[kslot(q0)], q0 / G::kSlotsK);
-        for (int j = t.lo; j < t.hi && ok; ++j) {
-          const int n = q0 + j - t.lo;
-          tc_fence_after_sync();
-          if (in0(j)) issue_s(0, qs0, kslot(n));
-          if (j > t.lo) {
-            if (in1(j - 1)) issue_pv(1, vslot(n - 1), j - 1 == t.lo1);
-            if (!ok) break;
-            commit(&bars->empty[vslot(n - 1)]);
-          }
-          if (in1(j)) issue_s(1, qs1, kslot(n));
-          commit(&bars->empty[kslot(n)]);
+        auto last_s = [&](int j) {   // after the S of block j
+          commit(&bars->empty[kslot(q0 + j - t.lo)]);
           if (j == t.hi - 1) {
             if (act0) commit(&bars->q_empty[qs0]);
             if (act1) commit(&bars->q_empty[qs1]);
           }
-          wait(&bars->full[vslot(n)], n / G::kSlotsV);
-          if (j + 1 < t.hi) wait(&bars->full[kslot(n + 1)], (n + 1) / G::kSlotsK);
-          if (!ok) break;
-          if (in0(j)) issue_pv(0, vslot(n), j == t.lo0);
-        }
-        if (ok) {
-          const int n = q0 + t.hi - 1 - t.lo;
-          tc_fence_after_sync();
-          if (in1(t.hi - 1)) issue_pv(1, vslot(n), t.hi - 1 == t.lo1);
-          if (ok) commit(&bars->empty[vslot(n)]);
+        };
+        if constexpr (kSplitP) {
+          // S0(j), S1(j), PV0(j-1), PV1(j-1)
+          for (int j = t.lo; j <= t.hi && ok; ++j) {
+            const int n = q0 + j - t.lo;
+            if (j < t.hi) {
+              wait(&bars->full[kslot(n)], n / G::kSlotsK);
+              if (ok && in0(j)) issue_s(0, qs0, kslot(n));
+              if (ok && in1(j)) issue_s(1, qs1, kslot(n));
+              if (!ok) break;
+              last_s(j);
+            }
+            if (j > t.lo) {
+              wait(&bars->full[vslot(n - 1)], (n - 1) / G::kSlotsV);
+              if (ok && in0(j - 1)) issue_pv(0, vslot(n - 1), j - 1 == t.lo0);
+              if (ok && in1(j - 1)) issue_pv(1, vslot(n - 1), j - 1 == t.lo1);
+              if (ok) commit(&bars->empty[vslot(n - 1)]);
+            }
+          }
+        } else {
+          // ping-pong: S0(j), PV1(j-1), S1(j), PV0(j); the fills of V(j) and
+          // K(j+1) are waited for before P0(j), the wait that lasts
+          wait(&bars->full[kslot(q0)], q0 / G::kSlotsK);
+          for (int j = t.lo; j < t.hi && ok; ++j) {
+            const int n = q0 + j - t.lo;
+            if (in0(j)) issue_s(0, qs0, kslot(n));
+            if (j > t.lo) {
+              if (in1(j - 1)) issue_pv(1, vslot(n - 1), j - 1 == t.lo1);
+              if (!ok) break;
+              commit(&bars->empty[vslot(n - 1)]);
+            }
+            if (in1(j)) issue_s(1, qs1, kslot(n));
+            if (!ok) break;
+            last_s(j);
+            wait(&bars->full[vslot(n)], n / G::kSlotsV);
+            if (j + 1 < t.hi) wait(&bars->full[kslot(n + 1)], (n + 1) / G::kSlotsK);
+            if (!ok) break;
+            if (in0(j)) issue_pv(0, vslot(n), j == t.lo0);
+          }
+          if (ok) {
+            const int n = q0 + t.hi - 1 - t.lo;
+            if (in1(t.hi - 1)) issue_pv(1, vslot(n), t.hi - 1 == t.lo1);
+            if (ok) commit(&bars->empty[vslot(n)]);
+          }
         }
       }
       q = q0 + t.hi - t.lo;
@@ -756,17 +961,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r_tok = r / p.group, r_head = r - (r / p.group) * p.group;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_base + u * 128u;
+    const uint32_t tP = kSplitP ? tmem + lane_base + 384u + u * 64u : tS;
     const uint32_t tO = tmem + lane_base + 256u + u * D;
     const uint32_t tO0 = tmem + lane_base + 256u;
     float2 *xch = reinterpret_cast<float2 *>(smem + PG::kOffXch);
     const float sl2 = p.scale_log2;
     const float2 sl2v = make_float2(sl2, sl2);
-    PagedPart t;
-    bool ok = true;
+    PagedItem t;
     int ns = 0;                              // S tiles taken so far
-    int nx = 0;                              // (m, l) hand-overs so far
+    int nx = 0;                              // (m, l) exchanges so far
+    int n_part = 0;                          // parts written so far
+    // one arrival for the warp, after its lanes' work
+    auto arrive = [&](uint64_t *bar) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(bar));
+    };
 
-    while (ok && walk.next(p, t)) {
+    for (int k = 0; ok && take(k, t); ++k) {
       const bool single = t.nt1 <= 0;
       const int tile = single ? 0 : u;       // query tile of this warpgroup
       const int nt = tile ? t.nt1 : t.nt0;
@@ -790,53 +1001,65 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = mbar_wait_warp(smem_u32(&bars->s_full[u]), ns & 1, abort_flag);
         if (!ok) break;
         tc_fence_after_sync();
-        if (busy) {
-        const bool full = k0 >= full_lo && k0 + kBN - 1 <= full_hi;
-        auto load_s = [&](float (&sv)[kBN]) {
-          uint32_t sr[4][32];
-          tmem_ld_x32(tS + 0, sr[0]);
-          tmem_ld_x32(tS + 32, sr[1]);
-          tmem_ld_x32(tS + 64, sr[2]);
-          tmem_ld_x32(tS + 96, sr[3]);
-          tmem_wait_ld();
-          reg_dep(sr[0]);
-          reg_dep(sr[1]);
-          reg_dep(sr[2]);
-          reg_dep(sr[3]);
-#pragma unroll
-          for (int c = 0; c < kBN; ++c) sv[c] = __uint_as_float(sr[c >> 5][c & 31]);
-          if (!full) {
-            const int lo_c = row_lo - k0, hi_c = row_hi - k0;
-#pragma unroll
-            for (int c = 0; c < kBN; ++c)
-              if (c < lo_c || c > hi_c) sv[c] = -INFINITY;
+        if (!busy) {
+          // nothing of this warp's rows is read or kept.  It must not arrive for
+          // this P while the others have not for the last one.
+          if (kSplitP) {
+            tc_fence_before_sync();
+            arrive(&bars->s_free[u]);
+            if (ns > 0) ok = mbar_wait_warp(smem_u32(&bars->pv_done[u]), (ns - 1) & 1, abort_flag);
+            if (!ok) break;
           }
-        };
-        // max first, the conditional rescale, then P
-        auto exact_pass = [&](float (&sv)[kBN]) {
-          float mx[4] = {sv[0], sv[1], sv[2], sv[3]};
+        } else {
+          const bool full = k0 >= full_lo && k0 + kBN - 1 <= full_hi;
+          auto load_s = [&](float (&sv)[kBN]) {
+            uint32_t sr[4][32];
+            tmem_ld_x32(tS + 0, sr[0]);
+            tmem_ld_x32(tS + 32, sr[1]);
+            tmem_ld_x32(tS + 64, sr[2]);
+            tmem_ld_x32(tS + 96, sr[3]);
+            tmem_wait_ld();
+            reg_dep(sr[0]);
+            reg_dep(sr[1]);
+            reg_dep(sr[2]);
+            reg_dep(sr[3]);
 #pragma unroll
-          for (int c = 4; c < kBN - 4; c += 8)
+            for (int c = 0; c < kBN; ++c) sv[c] = __uint_as_float(sr[c >> 5][c & 31]);
+            if (!full) {
+              const int lo_c = row_lo - k0, hi_c = row_hi - k0;
 #pragma unroll
-            for (int v = 0; v < 4; ++v) mx[v] = fmax3(mx[v], sv[c + 2 * v], sv[c + 2 * v + 1]);
-          const float m_blk = fmax3(fmax3(mx[0], mx[1], sv[kBN - 4]),
-                                    fmax3(mx[2], mx[3], sv[kBN - 3]),
-                                    fmaxf(sv[kBN - 2], sv[kBN - 1]));
-          const float m_new = (m_blk == -INFINITY) ? -INFINITY : m_blk * sl2;
+              for (int c = 0; c < kBN; ++c)
+                if (c < lo_c || c > hi_c) sv[c] = -INFINITY;
+            }
+          };
           float alpha = 1.0f;
-          const bool rescale = __any_sync(0xffffffffu, m_new > m_use + kRescaleThreshold);
-          if (rescale) {
-            const float m_upd = fmaxf(m_use, m_new);
-            alpha = (m_upd == -INFINITY) ? 1.0f : ex2(m_use - m_upd);
-            m_use = m_upd;
-            l *= alpha;
-          }
-          const float m_sub = (m_use == -INFINITY) ? 0.0f : m_use;
-          const float2 negm = make_float2(-m_sub, -m_sub);
-          float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          bool rescale = false;
+          float2 ls[2];
+          // the row's reference raised to m_new where some row of the warp
+          // grew by more than 2^8
+          auto raise = [&](float m_new) {
+            rescale = __any_sync(0xffffffffu, m_new > m_use + kRescaleThreshold);
+            if (rescale) {
+              const float m_upd = fmaxf(m_use, m_new);
+              alpha = (m_upd == -INFINITY) ? 1.0f : ex2(m_use - m_upd);
+              m_use = m_upd;
+              l *= alpha;
+            }
+          };
+          auto row_max = [&](const float (&sv)[kBN]) {
+            float mx[4] = {sv[0], sv[1], sv[2], sv[3]};
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint32_t pk[32];
+            for (int c = 4; c < kBN - 4; c += 8)
+#pragma unroll
+              for (int v = 0; v < 4; ++v) mx[v] = fmax3(mx[v], sv[c + 2 * v], sv[c + 2 * v + 1]);
+            const float m = fmax3(fmax3(mx[0], mx[1], sv[kBN - 4]), fmax3(mx[2], mx[3], sv[kBN - 3]),
+                                  fmaxf(sv[kBN - 2], sv[kBN - 1]));
+            return m == -INFINITY ? -INFINITY : m * sl2;
+          };
+          // P of one half against the reference; the weights summed unrounded
+          auto exp_half = [&](const float (&sv)[kBN], int half, uint32_t (&pk)[32]) {
+            const float m_sub = (m_use == -INFINITY) ? 0.0f : m_use;
+            const float2 negm = make_float2(-m_sub, -m_sub);
 #pragma unroll
             for (int c = 0; c < kBN / 2; c += 2) {
               const float2 e =
@@ -845,49 +1068,78 @@ __global__ void __launch_bounds__(kThreads, 1)
               ls[(c >> 1) & 1] = __fadd2_rn(ls[(c >> 1) & 1], pp);
               put_p<DT>(pk, c >> 1, pp.x, pp.y);
             }
-            store_p_half<DT>(tS, half, pk);
+          };
+          ls[0] = ls[1] = make_float2(0.f, 0.f);
+          if constexpr (kSplitP) {
+            float s[kBN];
+            load_s(s);
+            // S may be overwritten from here on; P and O wait for the PV before
+            tc_fence_before_sync();
+            arrive(&bars->s_free[u]);
+            raise(row_max(s));
+            uint32_t pk[2][32];
+            exp_half(s, 0, pk[0]);
+            exp_half(s, 1, pk[1]);
+            if (ns > 0) {
+              ok = mbar_wait_warp(smem_u32(&bars->pv_done[u]), (ns - 1) & 1, abort_flag);
+              if (!ok) break;
+              tc_fence_after_sync();
+            }
+            store_p_half<DT>(tP, 0, pk[0]);
+            store_p_half<DT>(tP, 1, pk[1]);
+            if (rescale && n > 0) scale_o_row<D>(tO, alpha);
+          } else {
+            auto exact_pass = [&](const float (&sv)[kBN]) {
+              raise(row_max(sv));
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                uint32_t pk[32];
+                exp_half(sv, half, pk);
+                store_p_half<DT>(tP, half, pk);
+              }
+              // O is complete up to the block before: S was issued after its PV
+              if (rescale && n > 0) scale_o_row<D>(tO, alpha);
+            };
+            // unmasked block, every row has a reference: exponentials and
+            // maximum side by side; redone if some row grew by more than 2^8
+            if (full && __all_sync(0xffffffffu, m_use != -INFINITY)) {
+              float s[kBN];
+              load_s(s);
+              const float2 negm = make_float2(-m_use, -m_use);
+              float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+              float2 lf[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+              uint32_t pk[2][32];
+#pragma unroll
+              for (int c = 0; c < kBN; c += 2) {
+                const int pair = c >> 1;
+                mx[pair & 3] = fmax3(mx[pair & 3], s[c], s[c + 1]);
+                const float2 e = __ffma2_rn(make_float2(s[c], s[c + 1]), sl2v, negm);
+                const float2 pp = make_float2(ex2(e.x), ex2(e.y));
+                lf[pair & 1] = __fadd2_rn(lf[pair & 1], pp);
+                put_p<DT>(pk[c >> 6], pair & 31, pp.x, pp.y);
+              }
+              const float m_new = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * sl2;
+              if (__any_sync(0xffffffffu, m_new > m_use + kRescaleThreshold)) {
+                float s2[kBN];
+                load_s(s2);
+                exact_pass(s2);
+              } else {
+                store_p_half<DT>(tP, 0, pk[0]);
+                store_p_half<DT>(tP, 1, pk[1]);
+                ls[0] = lf[0];
+                ls[1] = lf[1];
+              }
+            } else {
+              float s[kBN];
+              load_s(s);
+              exact_pass(s);
+            }
           }
           l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
-          // O is complete up to the block before: S was issued after its PV
-          if (rescale && n > 0) scale_o_row<D>(tO, alpha);
-        };
-        // unmasked block, every row has a reference: exponentials and maximum
-        // side by side; redone if some row's maximum grew by more than 2^8
-        if (full && __all_sync(0xffffffffu, m_use != -INFINITY)) {
-          float s[kBN];
-          load_s(s);
-          const float2 negm = make_float2(-m_use, -m_use);
-          float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          uint32_t pk[2][32];
-#pragma unroll
-          for (int c = 0; c < kBN; c += 2) {
-            const int pair = c >> 1;
-            mx[pair & 3] = fmax3(mx[pair & 3], s[c], s[c + 1]);
-            const float2 e = __ffma2_rn(make_float2(s[c], s[c + 1]), sl2v, negm);
-            const float2 pp = make_float2(ex2(e.x), ex2(e.y));
-            ls[pair & 1] = __fadd2_rn(ls[pair & 1], pp);
-            put_p<DT>(pk[c >> 6], pair & 31, pp.x, pp.y);
-          }
-          const float m_new = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * sl2;
-          if (__any_sync(0xffffffffu, m_new > m_use + kRescaleThreshold)) {
-            float s2[kBN];
-            load_s(s2);
-            exact_pass(s2);
-          } else {
-            store_p_half<DT>(tS, 0, pk[0]);
-            store_p_half<DT>(tS, 1, pk[1]);
-            l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
-          }
-        } else {
-          float s[kBN];
-          load_s(s);
-          exact_pass(s);
-        }
-        tmem_wait_st();
+          tmem_wait_st();
         }
         tc_fence_before_sync();
-        mbar_arrive(smem_u32(&bars->p_full[u]));
+        arrive(&bars->p_full[u]);
       }
       if (ok && n_blocks > 0) {
         ok = mbar_wait_warp(smem_u32(&bars->pv_done[u]), (ns - 1) & 1, abort_flag);
@@ -895,33 +1147,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
 
-      // ---- epilogue
+      // ---- epilogue.  A single tile: the warpgroups exchange their (m, l) and
+      // each joins every other 16 columns of the two O.
       float wa = 1.0f, wb = 0.0f;
-      bool both = false;
+      const bool two = single && t.hi - t.lo > 1;   // both O hold something
       if (single) {
-        // warpgroup 1 hands its (m, l) over; warpgroup 0 joins and writes
-        if (u == 1) {
-          if (nx > 0) ok = mbar_wait_warp(smem_u32(&bars->ml_free), (nx - 1) & 1, abort_flag);
-          if (!ok) break;
-          xch[r] = make_float2(m_use, l);
-          tc_fence_before_sync();
-          mbar_arrive(smem_u32(&bars->ml_full));
-          ++nx;
-          continue;
-        }
-        ok = mbar_wait_warp(smem_u32(&bars->ml_full), nx & 1, abort_flag);
+        if (nx > 0) ok = mbar_wait_warp(smem_u32(&bars->ml_free[u]), (nx - 1) & 1, abort_flag);
+        if (!ok) break;
+        xch[u * kBM + r] = make_float2(m_use, l);
+        tc_fence_before_sync();
+        arrive(&bars->ml_full[u]);
+        ok = mbar_wait_warp(smem_u32(&bars->ml_full[1 - u]), nx & 1, abort_flag);
         if (!ok) break;
         tc_fence_after_sync();
-        const float2 o = xch[r];
-        mbar_arrive(smem_u32(&bars->ml_free));
+        const float2 o = xch[(1 - u) * kBM + r];
+        arrive(&bars->ml_free[1 - u]);
         ++nx;
-        both = t.hi - t.lo > 1;
         const float m = fmaxf(m_use, o.x);
-        wa = (m_use == -INFINITY) ? 0.0f : ex2(m_use - m);
-        wb = (o.x == -INFINITY) ? 0.0f : ex2(o.x - m);
-        l = wa * l + wb * o.y;
+        const float w_mine = (m_use == -INFINITY) ? 0.0f : ex2(m_use - m);
+        const float w_other = (o.x == -INFINITY) ? 0.0f : ex2(o.x - m);
+        wa = u ? w_other : w_mine;
+        wb = u ? w_mine : w_other;
+        const float la = u ? o.y : l, lb = u ? l : o.y;
+        l = wa * la + wb * lb;       // the same sum in both warpgroups
         m_use = m;
       }
+      const bool none = t.hi <= t.lo || (!single && n_blocks <= 0);   // no O at all
       if (busy) {
         const float inv = t.slot >= 0 ? 1.0f : (l > 0.0f ? 1.0f / l : 0.0f);
         const int tok = t.tok0 + tile * p.tile_q + r_tok, head = t.h * p.group + r_head;
@@ -930,46 +1181,50 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint8_t *orow = static_cast<uint8_t *>(p.out) +
                         2 * (static_cast<long long>(tok) * p.out_st +
                              static_cast<long long>(head) * p.out_sh);
-        for_o_chunks<D>([&](int c, auto wd) {
-          constexpr int W = decltype(wd)::value;
-          uint32_t o[W];
-          if (n_blocks > 0) {
-            tmem_ld_cols<W>((single ? tO0 : tO) + c, o);
-            uint32_t o1[W];
-            if (both) tmem_ld_cols<W>(tO0 + D + c, o1);
-            tmem_wait_ld();
-            reg_dep(o);
-            if (both) {
+        float *wo = p.ws_o + wrow * D;
+        const uint32_t from = single ? tO0 : tO;
+        const float sa = wa * inv, sb = wb * inv;
+#pragma unroll 1
+        for (int c = single ? 16 * u : 0; c < D; c += single ? 32 : 16) {
+          uint32_t o[16];
+          if (none) {
+#pragma unroll
+            for (int v = 0; v < 16; ++v) o[v] = 0u;
+          } else {
+            tmem_ld_x16(from + c, o);
+            if (two) {
+              uint32_t o1[16];
+              tmem_ld_x16(from + D + c, o1);
+              tmem_wait_ld();
+              reg_dep(o);
               reg_dep(o1);
 #pragma unroll
-              for (int v = 0; v < W; ++v)
-                o[v] = __float_as_uint(wa * __uint_as_float(o[v]) + wb * __uint_as_float(o1[v]));
-            }
-          } else {
+              for (int v = 0; v < 16; ++v)
+                o[v] = __float_as_uint(sa * __uint_as_float(o[v]) + sb * __uint_as_float(o1[v]));
+            } else {
+              tmem_wait_ld();
+              reg_dep(o);
 #pragma unroll
-            for (int v = 0; v < W; ++v) o[v] = 0u;
+              for (int v = 0; v < 16; ++v) o[v] = __float_as_uint(sa * __uint_as_float(o[v]));
+            }
           }
           if (valid && t.slot >= 0) {
-            float4 *dst = reinterpret_cast<float4 *>(p.ws_o + wrow * D + c);
 #pragma unroll
-            for (int v = 0; v < W / 4; ++v)
-              dst[v] = make_float4(__uint_as_float(o[4 * v]), __uint_as_float(o[4 * v + 1]),
-                                   __uint_as_float(o[4 * v + 2]), __uint_as_float(o[4 * v + 3]));
+            for (int v = 0; v < 4; ++v)
+              *reinterpret_cast<float4 *>(wo + c + 4 * v) =
+                  make_float4(__uint_as_float(o[4 * v]), __uint_as_float(o[4 * v + 1]),
+                              __uint_as_float(o[4 * v + 2]), __uint_as_float(o[4 * v + 3]));
           } else if (valid) {
+            uint32_t w[8];
 #pragma unroll
-            for (int v = 0; v < W / 8; ++v) {
-              uint32_t w[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                w[e] = pack2<DT>(__uint_as_float(o[8 * v + 2 * e]) * inv,
-                                 __uint_as_float(o[8 * v + 2 * e + 1]) * inv);
-              *reinterpret_cast<uint4 *>(orow + 2 * c + 16 * v) =
-                  make_uint4(w[0], w[1], w[2], w[3]);
-            }
+            for (int v = 0; v < 8; ++v)
+              w[v] = pack2<DT>(__uint_as_float(o[2 * v]), __uint_as_float(o[2 * v + 1]));
+            *reinterpret_cast<uint4 *>(orow + 2 * c) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4 *>(orow + 2 * c + 16) = make_uint4(w[4], w[5], w[6], w[7]);
           }
           __syncwarp();   // the next chunk's load is warp-collective
-        });
-        if (valid) {
+        }
+        if (valid && !(single && u == 1)) {
           if (t.slot >= 0)
             p.ws_ml[wrow] = make_float2(l > 0.0f ? m_use : -INFINITY, l);
           else if (p.lse != nullptr)
@@ -977,11 +1232,43 @@ __global__ void __launch_bounds__(kThreads, 1)
                 l > 0.0f ? (m_use + __log2f(l)) * 0.6931471805599453f : -INFINITY;
         }
       }
-      // O has been read: the next item's first PV may overwrite it
-      if (n_blocks > 0) {
-        tc_fence_before_sync();
-        mbar_arrive(smem_u32(&bars->o_free[u]));
-        if (both) mbar_arrive(smem_u32(&bars->o_free[1]));
+      // O has been read: the next item's first PV may overwrite it.  (Eight
+      // arrivals: a pair's tile has one warpgroup, whose warps count twice.)
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        if (single) {
+          if (t.hi > t.lo) mbar_arrive(smem_u32(&bars->o_free[0]));
+          if (two) mbar_arrive(smem_u32(&bars->o_free[1]));
+        } else if (n_blocks > 0) {
+          mbar_arrive_n(smem_u32(&bars->o_free[u]), 2);
+        }
+      }
+      if (t.slot >= 0) {
+        // a part: whoever finishes the item's last one joins them all
+        __threadfence();
+        arrive(&bars->part_done);
+        if (tid == 0) {
+          ok = mbar_wait(smem_u32(&bars->part_done), n_part & 1, abort_flag);
+          if (ok) {
+            __threadfence();
+            bars->is_last = paged_ticket(p, t.cta0, t.parts);
+            bars->ticketed[t.slot] = 1;
+            __threadfence();
+            mbar_arrive(smem_u32(&bars->part_last));
+          }
+        }
+        __syncwarp();
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok) ok = mbar_wait_warp(smem_u32(&bars->part_last), n_part & 1, abort_flag);
+        if (!ok) break;
+        ++n_part;
+        if (bars->is_last) {
+          __threadfence();
+          paged_merge<D, DT>(p, t, warp, 8);
+        }
+        // (is_last is written again only after all eight warps have arrived
+        // for the next part)
       }
     }
   }
@@ -989,118 +1276,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   // ---- teardown
   tc_fence_before_sync();
   __syncthreads();
+  if (*abort_flag && warp == kSchedWarp) {
+    // every part is counted, so that the tickets end at 0 for the next call
+    PagedWalk walk;
+    PagedItem t;
+    walk.start(p, bars->setup, cuts);
+    while (walk.next(p, cuts, t))
+      if (t.slot >= 0 && lane == 0 && !bars->ticketed[t.slot]) paged_ticket(p, t.cta0, t.parts);
+  }
   if (warp == kMmaWarp) {
     tc_fence_after_sync();
     mbar_wait_slow(smem_u32(&bars->mma_done), 0, abort_flag, false);
     __syncwarp();
     tmem_dealloc(tmem, kTmemCols);
-  }
-}
-
-// ------------------------------------------------------------------ the merge
-// Joins the parts of an item that was cut: m = max_i m_i, w_i = 2^(m_i - m),
-// O = sum_i w_i O_i / sum_i w_i l_i, lse = (m + log2 l) ln 2.  blockIdx.x: the
-// CTA in whose piece the item ended.  Its parts lie in that CTA's slot 0, in
-// slot 0 of every earlier CTA wholly inside the item, and in slot 1 of the CTA
-// where it began; they are joined in that order, so the result does not depend
-// on timing.  Few parts: a warp per row; many (one long request): the warps
-// of a block share a row's parts.
-constexpr int kMergeThreads = 256;
-constexpr int kMergeY = 8;        // blocks per item
-constexpr int kMergeAlone = 8;    // parts a warp joins by itself
-
-template <int D, int DT>
-__global__ void __launch_bounds__(kMergeThreads)
-    fa_paged_merge_kernel(const __grid_constant__ PagedParams p) {
-  constexpr int kWarps = kMergeThreads / 32;
-  __shared__ float4 acc_s[kWarps][32];
-  __shared__ float l_s[kWarps];
-  const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const PagedRec rec = p.rec[c];
-  if (!rec.cont || !rec.ends) return;
-  // parts: CTAs c, c-1, ..., c-n+1; the walk back ends at the first CTA that
-  // does not lie wholly inside the item
-  int n = 1;
-  for (int back = 1; back <= c; back += 32) {
-    const int o = c - back - lane;
-    bool inside = false;
-    if (o >= 0) inside = p.rec[o].cont && !p.rec[o].ends;
-    const unsigned stop = ~__ballot_sync(0xffffffffu, inside);
-    if (stop) {
-      n = back + __ffs(stop);
-      break;
-    }
-  }
-  const PagedReq req = paged_req(p, rec.b);
-  const int i0 = rec.pair * 2 * p.tile_q;
-  const int nt0 = min(p.tile_q, req.q_len - i0);
-  const int nt1 = min(p.tile_q, req.q_len - i0 - nt0);
-  const int rows0 = nt0 * p.group, rows = rows0 + max(nt1, 0) * p.group;
-
-  auto slot_of = [&](int i) {   // slot of part i (0: the last)
-    return static_cast<size_t>(2 * (c - i) + (i == n - 1 ? 1 : 0)) * kPagedRows;
-  };
-  auto one_row = [&](int k, bool shared) {
-    const int tile = k >= rows0 ? 1 : 0, rr = k - tile * rows0;
-    const size_t in = static_cast<size_t>(tile) * kBM + rr;
-    float m = -INFINITY;
-    for (int i = lane; i < n; i += 32) m = fmaxf(m, p.ws_ml[slot_of(i) + in].x);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    const float m_sub = m == -INFINITY ? 0.0f : m;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.0f;
-    const int from = shared ? warp : 0, step = shared ? kWarps : 1;
-#pragma unroll 4
-    for (int i = from; i < n; i += step) {
-      const float2 ml = p.ws_ml[slot_of(i) + in];
-      const float w = exp2f(ml.x - m_sub);     // a part without a visible key: 0
-      l += w * ml.y;
-      if (lane * 4 < D) {
-        const float4 o = *reinterpret_cast<const float4 *>(p.ws_o + (slot_of(i) + in) * D + 4 * lane);
-        acc.x += w * o.x;
-        acc.y += w * o.y;
-        acc.z += w * o.z;
-        acc.w += w * o.w;
-      }
-    }
-    if (shared) {
-      acc_s[warp][lane] = acc;
-      if (lane == 0) l_s[warp] = l;
-      __syncthreads();
-      if (warp == 0) {
-        acc = acc_s[0][lane];
-        l = l_s[0];
-        for (int w = 1; w < kWarps; ++w) {
-          const float4 o = acc_s[w][lane];
-          acc.x += o.x;
-          acc.y += o.y;
-          acc.z += o.z;
-          acc.w += o.w;
-          l += l_s[w];
-        }
-      }
-    }
-    if (!shared || warp == 0) {
-      const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-      const int tok = req.q_start + i0 + tile * p.tile_q + rr / p.group;
-      const int head = rec.h * p.group + rr % p.group;
-      if (lane * 4 < D) {
-        uint2 *dst = reinterpret_cast<uint2 *>(
-            static_cast<uint8_t *>(p.out) + 2 * (static_cast<long long>(tok) * p.out_st +
-                                                 static_cast<long long>(head) * p.out_sh + 4 * lane));
-        *dst = make_uint2(pack2<DT>(acc.x * inv, acc.y * inv), pack2<DT>(acc.z * inv, acc.w * inv));
-      }
-      if (lane == 0 && p.lse != nullptr)
-        p.lse[static_cast<size_t>(tok) * p.H + head] =
-            l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
-    }
-    if (shared) __syncthreads();
-  };
-  if (n <= kMergeAlone) {
-    for (int k = blockIdx.y * kWarps + warp; k < rows; k += kMergeY * kWarps) one_row(k, false);
-  } else {
-    for (int k = blockIdx.y; k < rows; k += kMergeY) one_row(k, true);
   }
 }
 

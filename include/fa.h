@@ -470,14 +470,14 @@ int fa_qk_norm_rope_bwd(const fa_rope_args *args, fa_rows dq, fa_rows dk, float 
                         cudaStream_t stream);
 
 /* Workspace bytes of fa_fwd_paged on the current device (0 for an
- * unsupported D): two partial tiles of 256 rows for each SM.  They do not
- * depend on the batch. */
+ * unsupported D): two partial tiles of 256 rows and a counter for each SM.
+ * They do not depend on the batch. */
 size_t fa_paged_workspace_bytes(int D);
 
 /*
  * fa_fwd_paged -- exact attention of each request's new tokens over its
  * paged key/value cache, which holds the new tokens' keys and values too:
- * prefill chunks, single tokens (decoding) and mixtures, in two launches.
+ * prefill chunks, single tokens (decoding) and mixtures, in one launch.
  *
  *   q         device, rows of `dtype`: token t, head h at t * q_stride_t +
  *             h * q_stride_h; request b's new tokens are cu_q[b] ..
@@ -493,7 +493,7 @@ size_t fa_paged_workspace_bytes(int D);
  *             visible iff j < kv_len, j <= position + window_right (0 when
  *             causal), j >= position - window_left
  *   D         a multiple of 16 in [16, 128]; H / H_kv at most 128
- *   page_size 16, 32, 64 or a multiple of 128 (FA_ERR_ARG)
+ *   page_size a power of two, at least 16 (FA_ERR_ARG)
  *   workspace device, 256-byte aligned, at least fa_paged_workspace_bytes(D)
  *             bytes; contents on entry do not matter.  Calls that share a
  *             workspace must not overlap on the GPU.

@@ -55,9 +55,9 @@ def test_paged_empty_is_a_no_op(lib):
 
 
 def test_paged_workspace_bytes(lib):
-    # two tiles of 256 rows of D fp32 and a float2 for each SM, 32 bytes each
+    # two tiles of 256 rows of D fp32 and a float2, and a counter, for each SM
     sms = 148
-    assert fa.fa_paged_workspace_bytes(64) == sms * (2 * 256 * (64 * 4 + 8) + 32)
+    assert fa.fa_paged_workspace_bytes(64) == sms * (2 * 256 * (64 * 4 + 8) + 8)
     assert fa.fa_paged_workspace_bytes(40) == 0
 
 
