@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 import threading
 from typing import NamedTuple
 
@@ -117,7 +118,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.fa_bwd_ex.restype = i
         lib.fa_bwd_workspace_bytes.argtypes = [i, i, i, i]
         lib.fa_bwd_workspace_bytes.restype = ctypes.c_size_t
-        sz, pa = ctypes.c_size_t, ctypes.POINTER(FaRopeArgs)
+        sz, pa = ctypes.c_size_t, ctypes.c_void_p   # (a FaRopeArgs by reference, or its bytes)
         lib.fa_paged_plan.argtypes = [vp, vp, vp, ll, vp, i, i, i, i, i, vp, vp, vp, vp, vp, vp]
         lib.fa_paged_plan.restype = i
         lib.fa_qk_norm_rope.argtypes = [pa, vp]
@@ -652,6 +653,9 @@ def flash_fwd_host(q, k, v, scale=None, causal=False, window_left=-1, window_rig
 
 
 # ------------------------------------------------------------ serving
+# (These run once or more per layer of a decoding step, where a call's host
+# time counts: checks compare without copies, outputs come from few
+# allocations, the argument block is packed at once.)
 class PagedPlan(NamedTuple):
     """What paged_plan returns: device tensors of one serving step."""
     cu_q: "object"        # int32 [B + 1]
@@ -661,33 +665,33 @@ class PagedPlan(NamedTuple):
     counts: "object"      # int32 [3]: new tokens, pages taken, tokens without a slot
 
 
-class _on:
-    """The given device made current, if it is not already."""
+def _call(dev, stream, where, fn, *args):
+    """fn(*args, stream) with device `dev` current; raises on a status."""
+    import torch
 
-    def __init__(self, index):
-        self.index, self.back = index, None
-
-    def __enter__(self):
-        import torch
-        now = torch.cuda.current_device()
-        if now != self.index:
-            torch.cuda.set_device(self.index)
-            self.back = now
-
-    def __exit__(self, *exc):
-        import torch
-        if self.back is not None:
-            torch.cuda.set_device(self.back)
+    if stream is None:
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        handle = raw(dev) if raw is not None else torch.cuda.current_stream(dev).cuda_stream
+    else:
+        handle = stream.cuda_stream
+    if torch.cuda.current_device() == dev:
+        st = fn(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, handle)
+    if st != FA_OK:
+        raise FaError(st, where)
 
 
-def _same_device(index, **tensors):
-    for name, t in tensors.items():
-        if t is not None and (not t.is_cuda or t.device.index != index):
-            raise ValueError(f"{name} must be a CUDA tensor on the same device")
+def _on_device(dev, names, *tensors):
+    """Every tensor (None: not given) on CUDA device `dev`."""
+    for name, t in zip(names, tensors):
+        if t is not None and (dev < 0 or t.get_device() != dev):
+            raise ValueError(f"{name} must be a CUDA tensor on the same device as the others")
 
 
 def _vector(name, t, dtype, n):
-    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+    if t.dtype != dtype or t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} vector of {n}")
 
 
@@ -702,15 +706,26 @@ def _16bit(q):
 
 def _cache_layout(k_cache, v_cache, H_kv, D, dtype):
     """(pages, page size, element strides) of caches [pages, page_size, H_kv, D]."""
-    if k_cache.dim() != 4 or tuple(k_cache.shape) != tuple(v_cache.shape) \
-            or k_cache.shape[2] != H_kv or k_cache.shape[3] != D:
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape or shape[2] != H_kv or shape[3] != D:
         raise ValueError("k_cache, v_cache must be [pages, page_size, H_kv, D]")
     if k_cache.dtype != dtype or v_cache.dtype != dtype:
         raise TypeError("k_cache, v_cache must have q's dtype")
     st = k_cache.stride()
     if st != v_cache.stride() or st[3] != 1:
         raise ValueError("k_cache, v_cache must have the same strides, contiguous along D")
-    return k_cache.shape[0], k_cache.shape[1], st[0], st[1], st[2]
+    return shape[0], shape[1], st[0], st[1], st[2]
+
+
+def _table_layout(block_table, B):
+    """(columns, row stride) of a block table [B, max_pages]."""
+    import torch
+
+    if block_table.dim() != 2 or block_table.dtype != torch.int32 or block_table.shape[0] != B \
+            or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError("block_table must be int32 [B, max_pages], contiguous along the pages")
+    n = block_table.shape[1]
+    return n, block_table.stride(0) if B > 1 else max(n, 1)
 
 
 def paged_plan(q_lens, ctx_lens, block_table, free_pages, page_size, num_tokens, out=None,
@@ -721,89 +736,80 @@ def paged_plan(q_lens, ctx_lens, block_table, free_pages, page_size, num_tokens,
     the cache; block_table: int32 [B, max_pages] (rows may be strided), grown
     in place from free_pages (int32, taken from index 0); num_tokens: the
     capacity of positions and slots (at least the new tokens; the rest, a
-    captured graph's padding, gets -1).  ``out``: a PagedPlan to write into.
-    Nothing is read back: counts[2] > 0 tells that pages ran out."""
+    captured graph's padding, gets -1).  ``out``: a PagedPlan to write into;
+    otherwise its tensors share one allocation.  Nothing is read back:
+    counts[2] > 0 tells that pages ran out."""
     import torch
 
-    B = q_lens.shape[0]
+    if q_lens.dim() != 1 or free_pages.dim() != 1:
+        raise ValueError("q_lens and free_pages must be vectors")
+    B, T = q_lens.shape[0], int(num_tokens)
     i32 = torch.int32
     _vector("q_lens", q_lens, i32, B)
     _vector("ctx_lens", ctx_lens, i32, B)
-    if block_table.dim() != 2 or block_table.dtype != i32 or block_table.shape[0] != B \
-            or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
-        raise ValueError("block_table must be int32 [B, max_pages], contiguous along the pages")
-    _vector("free_pages", free_pages, i32, free_pages.numel())
-    dev = q_lens.device.index
-    _same_device(dev, q_lens=q_lens, ctx_lens=ctx_lens, block_table=block_table,
-                 free_pages=free_pages)
-    num_tokens = int(num_tokens)
+    n_free = free_pages.shape[0]
+    _vector("free_pages", free_pages, i32, n_free)
+    max_pages, table_stride = _table_layout(block_table, B)
+    dev = q_lens.get_device()
+    _on_device(dev, ("q_lens", "ctx_lens", "block_table", "free_pages"), q_lens, ctx_lens,
+               block_table, free_pages)
     if out is None:
-        if num_tokens < 0:
+        if T < 0:
             raise ValueError("num_tokens must be >= 0")
-        d = q_lens.device
-        out = PagedPlan(torch.empty(B + 1, dtype=i32, device=d), torch.empty(B, dtype=i32, device=d),
-                        torch.empty(num_tokens, dtype=i32, device=d),
-                        torch.empty(num_tokens, dtype=torch.int64, device=d),
-                        torch.empty(3, dtype=i32, device=d))
+        # slots first: 8-byte values at the start of the allocation
+        buf = q_lens.new_empty(2 * T + T + 2 * B + 4)
+        slots, positions, cu_q, kv_lens, counts = buf.split((2 * T, T, B + 1, B, 3))
+        out = PagedPlan(cu_q, kv_lens, positions, slots.view(torch.int64), counts)
     else:
-        for name, dt, n in (("cu_q", i32, B + 1), ("kv_lens", i32, B), ("positions", i32, num_tokens),
-                            ("slots", torch.int64, num_tokens), ("counts", i32, 3)):
+        for name, dt, n in (("cu_q", i32, B + 1), ("kv_lens", i32, B), ("positions", i32, T),
+                            ("slots", torch.int64, T), ("counts", i32, 3)):
             _vector(name, getattr(out, name), dt, n)
-        _same_device(dev, **out._asdict())
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    max_pages = block_table.shape[1]
-    with _on(dev):
-        st = fa_paged_plan(q_lens.data_ptr(), ctx_lens.data_ptr(), block_table.data_ptr(),
-                           block_table.stride(0) if B > 1 else max(max_pages, 1),
-                           free_pages.data_ptr(), free_pages.shape[0], B, max_pages,
-                           int(page_size), num_tokens, out.cu_q.data_ptr(),
-                           out.kv_lens.data_ptr(), out.positions.data_ptr(),
-                           out.slots.data_ptr(), out.counts.data_ptr(), stream.cuda_stream)
-    if st != FA_OK:
-        raise FaError(st, "fa_paged_plan")
+        _on_device(dev, PagedPlan._fields, *out)
+    lib = _lib or load()
+    _call(dev, stream, "fa_paged_plan", lib.fa_paged_plan, q_lens.data_ptr(), ctx_lens.data_ptr(),
+          block_table.data_ptr(), table_stride, free_pages.data_ptr(), n_free, B, max_pages,
+          int(page_size), T, out.cu_q.data_ptr(), out.kv_lens.data_ptr(),
+          out.positions.data_ptr(), out.slots.data_ptr(), out.counts.data_ptr())
     return out
 
 
 def _rows(name, t, shape, dtype):
-    """fa_rows of a [T, H, D] or [B, L, H, D] tensor of the given shape."""
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.stride(-1) != 1:
-        raise ValueError(f"{name} must be {tuple(shape)}, {dtype}, contiguous along D")
+    """fa_rows of a [T, H, D] or [B, L, H, D] tensor of the given shape, as a tuple."""
     s = t.stride()
-    return FaRows(t.data_ptr(), s[0] if len(s) == 4 else 0, s[-3], s[-2])
+    if t.shape != shape or t.dtype != dtype or s[-1] != 1:
+        raise ValueError(f"{name} must be {tuple(shape)}, {dtype}, contiguous along D")
+    return t.data_ptr(), (s[0] if len(s) == 4 else 0), s[-3], s[-2]
 
 
-def _rope_args(q, k, q_weight, k_weight, cos_sin, positions, eps, interleaved):
+_NO_ROWS = (0, 0, 0, 0)
+_NO_CACHE = (0, 0, 0, 0, 0, 0)
+_PACK_ROPE = struct.Struct("@32q12if4x")   # FaRopeArgs
+
+
+def _rope_common(q, k, q_weight, k_weight, cos_sin, positions):
+    """Checks shared by both directions: (dims, pointers) of fa_rope_args."""
     import torch
 
-    if q.dim() not in (3, 4) or k.dim() != q.dim() or k.shape[:-2] != q.shape[:-2] \
-            or k.shape[-1] != q.shape[-1]:
+    qs, ks = q.shape, k.shape
+    if len(qs) not in (3, 4) or len(ks) != len(qs) or ks[:-2] != qs[:-2] or ks[-1] != qs[-1]:
         raise ValueError("q, k must be [T, H, D] and [T, H_kv, D], or [B, L, H, D] and "
                          "[B, L, H_kv, D]")
-    a = FaRopeArgs()
-    a.dtype = _16bit(q)
-    a.B = q.shape[0] if q.dim() == 4 else 1
-    a.L, a.H, a.D = q.shape[-3:]
-    a.H_kv = k.shape[-2]
-    a.q = _rows("q", q, q.shape, q.dtype)
-    a.k = _rows("k", k, k.shape, q.dtype)
+    dtype, D = _16bit(q), qs[-1]
     for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
         if w is not None:
-            _vector(name, w, q.dtype, a.D)
-            setattr(a, name, w.data_ptr())
+            _vector(name, w, q.dtype, D)
     if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32 or not cos_sin.is_contiguous():
         raise ValueError("cos_sin must be a contiguous float32 [max_pos, rot_dim]")
-    a.max_pos, a.rot_dim = cos_sin.shape
-    a.cos_sin = cos_sin.data_ptr()
-    if positions.shape != q.shape[:-2] or positions.dtype not in (torch.int32, torch.int64):
+    wide = positions.dtype == torch.int64
+    if positions.shape != qs[:-2] or not (wide or positions.dtype == torch.int32):
         raise ValueError("positions must be int32 or int64 of q's token axes")
-    a.positions = positions.data_ptr()
-    a.positions_64 = int(positions.dtype == torch.int64)
     ps = positions.stride()
-    a.positions_stride_b, a.positions_stride_l = (ps[0] if len(ps) == 2 else 0), ps[-1]
-    a.eps = eps
-    a.interleaved = int(interleaved)
-    return a
+    max_pos, rot = cos_sin.shape
+    ptrs = (0 if q_weight is None else q_weight.data_ptr(),
+            0 if k_weight is None else k_weight.data_ptr(), cos_sin.data_ptr(),
+            positions.data_ptr(), ps[0] if len(ps) == 2 else 0, ps[-1])
+    dims = (int(wide), qs[0] if len(qs) == 4 else 1, qs[-3], qs[-2], ks[-2], D, rot, max_pos)
+    return dtype, dims, ptrs
 
 
 def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps=1e-6, interleaved=False,
@@ -827,35 +833,31 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps=1e-6, interle
     given.  Returns (q_out, k_out)."""
     import torch
 
-    a = _rope_args(q, k, q_weight, k_weight, cos_sin, positions, eps, interleaved)
-    dev = q.device.index
+    dtype, dims, ptrs = _rope_common(q, k, q_weight, k_weight, cos_sin, positions)
+    rows_v, cache, pages, page_size = _NO_ROWS, _NO_CACHE, 0, 0
     cached = k_cache is not None or v_cache is not None
     if cached:
         if k_cache is None or v_cache is None or v is None or slots is None:
             raise ValueError("a cache needs k_cache, v_cache, v and slots")
-        a.num_pages, a.page_size, a.cache_stride_page, a.cache_stride_token, \
-            a.cache_stride_head = _cache_layout(k_cache, v_cache, a.H_kv, a.D, q.dtype)
-        a.k_cache, a.v_cache = k_cache.data_ptr(), v_cache.data_ptr()
-        a.v = _rows("v", v, k.shape, q.dtype)
-        if slots.dtype != torch.int64 or slots.numel() != a.B * a.L or not slots.is_contiguous():
+        pages, page_size, sp, st, sh = _cache_layout(k_cache, v_cache, dims[4], dims[5], q.dtype)
+        rows_v = _rows("v", v, k.shape, q.dtype)
+        if slots.dtype != torch.int64 or slots.numel() != dims[1] * dims[2] \
+                or not slots.is_contiguous():
             raise ValueError("slots must be contiguous int64, one per token")
-        a.slots = slots.data_ptr()
-    _same_device(dev, q=q, k=k, q_weight=q_weight, k_weight=k_weight, cos_sin=cos_sin,
-                 positions=positions, q_out=q_out, k_out=k_out, v=v, k_cache=k_cache,
-                 v_cache=v_cache, slots=slots)
+        cache = (k_cache.data_ptr(), v_cache.data_ptr(), sp, st, sh, slots.data_ptr())
+    dev = q.get_device()
+    _on_device(dev, ("q", "k", "q_weight", "k_weight", "cos_sin", "positions", "q_out", "k_out", "v",
+                     "k_cache", "v_cache", "slots"), q, k, q_weight, k_weight, cos_sin, positions,
+               q_out, k_out, v, k_cache, v_cache, slots)
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    a.q_out = _rows("q_out", q_out, q.shape, q.dtype)
+        q_out = q.new_empty(q.shape)
     if k_out is None and not cached:
-        k_out = torch.empty(k.shape, dtype=q.dtype, device=q.device)
-    if k_out is not None:
-        a.k_out = _rows("k_out", k_out, k.shape, q.dtype)
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    with _on(dev):
-        st = fa_qk_norm_rope(a, stream.cuda_stream)
-    if st != FA_OK:
-        raise FaError(st, "fa_qk_norm_rope")
+        k_out = q.new_empty(k.shape)
+    rows_ko = _NO_ROWS if k_out is None else _rows("k_out", k_out, k.shape, q.dtype)
+    args = _PACK_ROPE.pack(*_rows("q", q, q.shape, q.dtype), *_rows("k", k, k.shape, q.dtype),
+                           *rows_v, *_rows("q_out", q_out, q.shape, q.dtype), *rows_ko, *ptrs,
+                           *cache, pages, page_size, *dims, int(interleaved), dtype, eps)
+    _call(dev, stream, "fa_qk_norm_rope", (_lib or load()).fa_qk_norm_rope, args)
     return q_out, k_out
 
 
@@ -868,34 +870,34 @@ def qk_norm_rope_bwd(q, k, q_weight, k_weight, cos_sin, positions, dq_out, dk_ou
     here unless given (a uint8 CUDA tensor, 256-byte aligned)."""
     import torch
 
-    a = _rope_args(q, k, q_weight, k_weight, cos_sin, positions, eps, interleaved)
-    dev = q.device.index
-    a.q_out = _rows("dq_out", dq_out, q.shape, q.dtype)
-    a.k_out = _rows("dk_out", dk_out, k.shape, q.dtype)
-    _same_device(dev, q=q, k=k, q_weight=q_weight, k_weight=k_weight, cos_sin=cos_sin,
-                 positions=positions, dq_out=dq_out, dk_out=dk_out, dq=dq, dk=dk,
-                 workspace=workspace)
+    dtype, dims, ptrs = _rope_common(q, k, q_weight, k_weight, cos_sin, positions)
+    dev = q.get_device()
+    _on_device(dev, ("q", "k", "q_weight", "k_weight", "cos_sin", "positions", "dq_out", "dk_out",
+                     "dq", "dk", "workspace"), q, k, q_weight, k_weight, cos_sin, positions, dq_out,
+               dk_out, dq, dk, workspace)
     if dq is None:
-        dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        dq = q.new_empty(q.shape)
     if dk is None:
-        dk = torch.empty(k.shape, dtype=q.dtype, device=q.device)
-    rq, rk = _rows("dq", dq, q.shape, q.dtype), _rows("dk", dk, k.shape, q.dtype)
-    dwq = dwk = None
-    if q_weight is not None:
-        dwq = torch.empty(a.D, dtype=torch.float32, device=q.device)
-    if k_weight is not None:
-        dwk = torch.empty(a.D, dtype=torch.float32, device=q.device)
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    with _on(dev):
-        if workspace is None:
-            workspace = torch.empty(max(fa_qk_norm_rope_bwd_workspace_bytes(a.D), 1),
-                                    dtype=torch.uint8, device=q.device)
-        st = fa_qk_norm_rope_bwd(a, rq, rk, dwq.data_ptr() if dwq is not None else None,
-                                 dwk.data_ptr() if dwk is not None else None,
-                                 workspace.data_ptr(), workspace.numel(), stream.cuda_stream)
-    if st != FA_OK:
-        raise FaError(st, "fa_qk_norm_rope_bwd")
+        dk = q.new_empty(k.shape)
+    args = _PACK_ROPE.pack(*_rows("q", q, q.shape, q.dtype), *_rows("k", k, k.shape, q.dtype),
+                           *_NO_ROWS, *_rows("dq_out", dq_out, q.shape, q.dtype),
+                           *_rows("dk_out", dk_out, k.shape, q.dtype), *ptrs, *_NO_CACHE, 0, 0,
+                           *dims, int(interleaved), dtype, eps)
+    rq, rk = FaRows(*_rows("dq", dq, q.shape, q.dtype)), FaRows(*_rows("dk", dk, k.shape, q.dtype))
+    D = dims[5]
+    dwq = q.new_empty(D, dtype=torch.float32) if q_weight is not None else None
+    dwk = q.new_empty(D, dtype=torch.float32) if k_weight is not None else None
+    lib = _lib or load()
+
+    def run(handle):
+        ws = workspace
+        if ws is None:   # (sized for the current device)
+            ws = q.new_empty(max(lib.fa_qk_norm_rope_bwd_workspace_bytes(D), 1), dtype=torch.uint8)
+        return lib.fa_qk_norm_rope_bwd(args, rq, rk, None if dwq is None else dwq.data_ptr(),
+                                       None if dwk is None else dwk.data_ptr(), ws.data_ptr(),
+                                       ws.numel(), handle)
+
+    _call(dev, stream, "fa_qk_norm_rope_bwd", run)
     return dq, dk, dwq, dwk
 
 
@@ -916,49 +918,49 @@ def flash_fwd_paged(q, k_cache, v_cache, block_table, cu_q, kv_lens, scale=None,
     request owns are not written."""
     import torch
 
-    if q.dim() != 3 or q.stride(2) != 1:
+    qst = q.stride()
+    if len(qst) != 3 or qst[2] != 1:
         raise ValueError("q must be [total_q, H, D], contiguous along D")
     T, H, D = q.shape
     dtype = _16bit(q)
-    if k_cache.dim() != 4:
-        raise ValueError("k_cache, v_cache must be [pages, page_size, H_kv, D]")
+    if k_cache.dim() != 4 or kv_lens.dim() != 1:
+        raise ValueError("k_cache, v_cache must be [pages, page_size, H_kv, D], kv_lens a vector")
     H_kv = k_cache.shape[2]
-    pages, page_size, sp, st_, sh = _cache_layout(k_cache, v_cache, H_kv, D, q.dtype)
+    pages, page_size, sp, st, sh = _cache_layout(k_cache, v_cache, H_kv, D, q.dtype)
     B = kv_lens.shape[0]
     _vector("kv_lens", kv_lens, torch.int32, B)
     _vector("cu_q", cu_q, torch.int32, B + 1)
-    if block_table.dim() != 2 or block_table.dtype != torch.int32 or block_table.shape[0] != B \
-            or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
-        raise ValueError("block_table must be int32 [B, max_pages], contiguous along the pages")
-    dev = q.device.index
-    _same_device(dev, q=q, k_cache=k_cache, v_cache=v_cache, block_table=block_table, cu_q=cu_q,
-                 kv_lens=kv_lens, out=out, lse=lse, workspace=workspace)
+    max_pages, table_stride = _table_layout(block_table, B)
+    dev = q.get_device()
+    _on_device(dev, ("q", "k_cache", "v_cache", "block_table", "cu_q", "kv_lens", "out", "lse",
+                     "workspace"), q, k_cache, v_cache, block_table, cu_q, kv_lens, out, lse,
+               workspace)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     if out is None:
-        out = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
-    elif tuple(out.shape) != (T, H, D) or out.dtype != q.dtype or out.stride(2) != 1:
+        out = q.new_empty((T, H, D))
+    elif out.shape != q.shape or out.dtype != q.dtype or out.stride(2) != 1:
         raise ValueError("out must be like q, contiguous along D")
     if not return_lse:
         lse = None
     elif lse is None:
-        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
-    elif tuple(lse.shape) != (T, H) or lse.dtype != torch.float32 or not lse.is_contiguous():
+        lse = q.new_empty((T, H), dtype=torch.float32)
+    elif lse.shape != (T, H) or lse.dtype != torch.float32 or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous float32 [total_q, H]")
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    with _on(dev):
-        if workspace is None:
-            workspace = torch.empty(max(fa_paged_workspace_bytes(D), 1), dtype=torch.uint8,
-                                    device=q.device)
-        max_pages = block_table.shape[1]
-        st = fa_fwd_paged(q.data_ptr(), q.stride(0), q.stride(1), k_cache.data_ptr(),
-                          v_cache.data_ptr(), sp, st_, sh, block_table.data_ptr(),
-                          block_table.stride(0) if B > 1 else max_pages, cu_q.data_ptr(),
-                          kv_lens.data_ptr(), out.data_ptr(), out.stride(0), out.stride(1),
-                          lse.data_ptr() if lse is not None else None, T, B, H, H_kv, D, pages,
-                          page_size, max_pages, scale, causal, window_left, window_right, dtype,
-                          workspace.data_ptr(), workspace.numel(), stream.cuda_stream)
-    if st != FA_OK:
-        raise FaError(st, "fa_fwd_paged")
+    ost = out.stride()
+    lib = _lib or load()
+
+    def run(handle):
+        ws = workspace
+        if ws is None:   # (sized for the current device)
+            ws = q.new_empty(max(lib.fa_paged_workspace_bytes(D), 1), dtype=torch.uint8)
+        return lib.fa_fwd_paged(q.data_ptr(), qst[0], qst[1], k_cache.data_ptr(),
+                                v_cache.data_ptr(), sp, st, sh, block_table.data_ptr(),
+                                table_stride, cu_q.data_ptr(), kv_lens.data_ptr(), out.data_ptr(),
+                                ost[0], ost[1], None if lse is None else lse.data_ptr(), T, B, H,
+                                H_kv, D, pages, page_size, max_pages, scale, bool(causal),
+                                window_left, window_right, dtype, ws.data_ptr(), ws.numel(),
+                                handle)
+
+    _call(dev, stream, "fa_fwd_paged", run)
     return out, lse
