@@ -171,6 +171,8 @@ extern "C" int fa_fwd_paged(const void *q, long long q_stride_t, long long q_str
   p.out = out;
   p.out_st = out_stride_t;
   p.out_sh = out_stride_h;
+  p.out_wide = al(out, 32) && (total_q <= 1 || out_stride_t % 16 == 0) &&
+               (H <= 1 || out_stride_h % 16 == 0);
   p.lse = lse;
   p.B = B;
   p.H = H;

@@ -58,6 +58,7 @@ struct PagedParams {
   const int *kv_lens;
   void *out;
   long long out_st, out_sh;   // element strides of a token and a head
+  int out_wide;               // every row 32-byte aligned
   float *lse;                 // [total_q, H] or nullptr
   int B, H, H_kv, group, total_q;
   int tile_q;                 // tokens per tile
@@ -65,7 +66,7 @@ struct PagedParams {
   int box_rows;               // rows of one K/V copy: min(page size, 128)
   int wl, wr;                 // -1 = unbounded
   float scale_log2;
-  float *ws_o;                // [2 * grid][kPagedRows][D]
+  float *ws_o;                // [2 * grid][D / 4][kPagedRows][4]
   float2 *ws_ml;              // [2 * grid][kPagedRows]
   unsigned long long *ticket; // [grid]
   unsigned long long call;    // this call's number, 48 bits, not 0
@@ -111,6 +112,25 @@ __device__ __forceinline__ int paged_blocks(const PagedParams &p, const PagedReq
   return khi < klo ? 0 : khi / kBN - klo / kBN + 1;
 }
 
+// Cost of an item on the work line: a block of a pair takes about twice as
+// long as one of a single tile (2.2 against 1.2 us at D 128), and an item about
+// a block more.  before(off): the item's blocks that lie before a cut at off.
+struct PagedCost {
+  int blocks, per, cost;   // cost = per * (blocks + 1)
+  __device__ __forceinline__ int before(int off) const {
+    return off >= cost ? blocks : max((per == 2 ? off >> 1 : off) - 1, 0);
+  }
+  // the largest off before which no block lies
+  __device__ __forceinline__ int snap() const { return 2 * per - 1; }
+};
+__device__ __forceinline__ PagedCost paged_cost(const PagedParams &p, const PagedReq &r, int pair) {
+  PagedCost c;
+  c.blocks = paged_blocks(p, r, pair);
+  c.per = r.q_len - pair * 2 * p.tile_q > p.tile_q ? 2 : 1;
+  c.cost = c.per * (c.blocks + 1);
+  return c;
+}
+
 // Cost of one K/V head of a request; the whole warp calls it, each lane with
 // its own request (q_len 0: none).  Long requests are summed by all lanes.
 __device__ __forceinline__ long long paged_head_cost(const PagedParams &p, const PagedReq &r) {
@@ -119,7 +139,7 @@ __device__ __forceinline__ long long paged_head_cost(const PagedParams &p, const
   const int np = paged_pairs(p, r.q_len);
   long long sum = 0;
   if (np <= kAlone)
-    for (int i = 0; i < np; ++i) sum += paged_blocks(p, r, i) + 1;
+    for (int i = 0; i < np; ++i) sum += paged_cost(p, r, i).cost;
   unsigned todo = __ballot_sync(0xffffffffu, np > kAlone);
   while (todo) {
     const int src = __ffs(todo) - 1;
@@ -130,7 +150,7 @@ __device__ __forceinline__ long long paged_head_cost(const PagedParams &p, const
     o.kv_len = __shfl_sync(0xffffffffu, r.kv_len, src);
     const int n = paged_pairs(p, o.q_len);
     long long all = 0;
-    for (int i = lane; i < n; i += 32) all += paged_blocks(p, o, i) + 1;
+    for (int i = lane; i < n; i += 32) all += paged_cost(p, o, i).cost;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) all += __shfl_xor_sync(0xffffffffu, all, d);
     if (lane == src) sum = all;
@@ -145,6 +165,7 @@ struct PagedSetup {
   long long rest[2];      // units of the piece's ends within their request
   long long per_head[2];  // cost of one K/V head of that request
   int b[2];               // that request (B: the end of the line)
+  long long end;          // the piece's end, moved to a border where it has to
 };
 
 // a / b of non-negative numbers: in 32 bits where they fit (a quarter of the
@@ -254,7 +275,10 @@ struct PagedItem {
   int first, kv_len, lo, hi; // position of the first token; key blocks of the part
   int lo0, hi0, lo1, hi1;    // ... of each tile
   int klo, khi, slot, b;     // keys some token of the item sees; -1: the whole item, else the part's slot
-  int cta0, parts, pad[2];   // a cut item: the CTA where it began, its parts
+};
+// A cut item of this CTA (slot 0, slot 1): the CTA where it began, its parts.
+struct PagedCut {
+  int cta0, parts;
 };
 
 // Walks a CTA's piece (one warp).
@@ -262,10 +286,11 @@ struct PagedWalk {
   int b, h, pair, off;
   long long u, end;          // on the work line: here, and the piece's end
   PagedReq r;
+  long long began;           // of the item given last: its start, its cost
+  PagedCost cost;
 
-  // The place and cost of the item at end e of the piece; u moved to the border
-  // where a cut one unit behind an item's start would leave a part without a
-  // key block, and where it would leave the next part only the last one.
+  // The place of end e of the piece; `at` moved back to the item's start where
+  // no block of it lies before the cut.  All lanes.
   __device__ __forceinline__ void locate(const PagedParams &p, const PagedSetup &st, int e,
                                          long long &at) {
     const int lane = threadIdx.x & 31;
@@ -276,38 +301,35 @@ struct PagedWalk {
     const int np = paged_pairs(p, r.q_len);
     h = static_cast<int>(paged_div(st.rest[e], st.per_head[e]));
     long long in = st.rest[e] - h * st.per_head[e];
-    int cost = 0;
-    for (int base = 0; base < np; base += 32) {
-      const int i = base + lane;
-      const int cst = i < np ? paged_blocks(p, r, i) + 1 : 0;
-      long long incl = cst;
+    if (np > 1) {
+      for (int base = 0; base < np; base += 32) {
+        const int i = base + lane;
+        const long long cst = i < np ? paged_cost(p, r, i).cost : 0;
+        long long incl = cst;
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, incl, d);
-        if (lane >= d) incl += v;
+        for (int d = 1; d < 32; d <<= 1) {
+          const long long v = __shfl_up_sync(0xffffffffu, incl, d);
+          if (lane >= d) incl += v;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, incl > in);
+        if (hit) {
+          const int src = __ffs(hit) - 1;
+          pair = base + src;
+          in -= __shfl_sync(0xffffffffu, incl - cst, src);
+          break;
+        }
+        in -= __shfl_sync(0xffffffffu, incl, 31);
       }
-      const unsigned hit = __ballot_sync(0xffffffffu, incl > in);
-      if (hit) {
-        const int src = __ffs(hit) - 1;
-        pair = base + src;
-        cost = __shfl_sync(0xffffffffu, cst, src);
-        off = static_cast<int>(in - (__shfl_sync(0xffffffffu, incl, src) - cost));
-        break;
-      }
-      in -= __shfl_sync(0xffffffffu, incl, 31);
     }
-    if (off == 1) {
+    off = static_cast<int>(in);
+    if (paged_cost(p, r, pair).before(off) == 0) {
+      at -= off;
       off = 0;
-      at -= 1;
-    } else if (off == cost - 1 && off > 0) {
-      at += 1;
-      advance(p);
     }
   }
   __device__ __forceinline__ void start(const PagedParams &p, const PagedSetup &st,
                                         const PagedCuts &cuts) {
-    end = cuts.at(blockIdx.x + 1);
-    locate(p, st, 1, end);
+    end = st.end;
     u = cuts.at(blockIdx.x);
     locate(p, st, 0, u);
   }
@@ -322,7 +344,7 @@ struct PagedWalk {
       if (r.q_len > 0) return;
     }
   }
-  __device__ __forceinline__ bool next(const PagedParams &p, const PagedCuts &cuts, PagedItem &t) {
+  __device__ __forceinline__ bool next(const PagedParams &p, PagedItem &t) {
     if (u >= end || b >= p.B) {
       t.h = -1;
       return false;
@@ -335,34 +357,40 @@ struct PagedWalk {
     t.nt1 = min(p.tile_q, r.q_len - i0 - t.nt0);
     t.first = r.kv_len - r.q_len + i0;
     t.kv_len = r.kv_len;
-    int klo0, khi0, klo1, khi1;
+    int klo0, khi0, klo1 = 0, khi1 = -1;
     paged_keys(p, r, i0, t.nt0, klo0, khi0);
-    paged_keys(p, r, i0 + p.tile_q, t.nt1, klo1, khi1);
-    paged_keys(p, r, i0, t.nt0 + t.nt1, t.klo, t.khi);
-    const int blocks = t.khi < t.klo ? 0 : t.khi / kBN - t.klo / kBN + 1;
+    t.klo = klo0;
+    t.khi = khi0;
+    if (t.nt1 > 0) {
+      paged_keys(p, r, i0 + p.tile_q, t.nt1, klo1, khi1);
+      paged_keys(p, r, i0, t.nt0 + t.nt1, t.klo, t.khi);
+    }
+    const PagedCost c = paged_cost(p, r, pair);
     const int lo = t.klo / kBN;
-    const int cost = blocks + 1;
-    const int to = static_cast<int>(min(static_cast<long long>(cost), off + (end - u)));
-    t.lo = lo + max(off - 1, 0);
-    t.hi = to >= cost ? lo + blocks : lo + to - 1;
-    t.slot = off > 0 ? 0 : (to < cost ? 1 : -1);
+    const int to = static_cast<int>(min(static_cast<long long>(c.cost), off + (end - u)));
+    t.lo = lo + c.before(off);
+    t.hi = lo + c.before(to);
+    t.slot = off > 0 ? 0 : (to < c.cost ? 1 : -1);
     t.lo0 = max(t.lo, klo0 / kBN);
     t.hi0 = khi0 < klo0 ? t.lo0 : max(t.lo0, min(t.hi, khi0 / kBN + 1));
     t.lo1 = max(t.lo, klo1 / kBN);
     t.hi1 = khi1 < klo1 ? t.lo1 : max(t.lo1, min(t.hi, khi1 / kBN + 1));
-    t.cta0 = t.parts = 0;
-    if (t.slot >= 0) {
-      // the first and the last piece with a part of the item, by the cuts
-      // before they move to the borders (see locate)
-      t.cta0 = cuts.last(u - off + 1);
-      t.parts = cuts.last(u - off + cost - 2) - t.cta0 + 1;
-    }
+    began = u - off;
+    cost = c;
     u += to - off;
-    if (to >= cost)
+    if (to >= c.cost)
       advance(p);
     else
       off = to;
     return true;
+  }
+  // Of the item that next() gave last, by the cuts before they move to borders
+  // (a 64-bit division or two: its readers need it only when they are done).
+  __device__ __forceinline__ PagedCut cut_of(const PagedCuts &cuts) const {
+    PagedCut k;
+    k.cta0 = cuts.last(began + cost.snap());
+    k.parts = cuts.last(began + cost.cost - 1) - k.cta0 + 1;
+    return k;
   }
 };
 
@@ -383,6 +411,7 @@ struct PagedBars {
   uint64_t o_free[2];    // O_t has been read by the epilogue
   uint64_t ml_full[2];   // single tile: warpgroup's (m, l) written
   uint64_t ml_free[2];   // ... and read
+  uint64_t cut_full[2];  // cut[slot] written
   uint64_t part_done;    // a part's rows are in the workspace
   uint64_t part_last;    // whether they were the item's last is known
   uint64_t mma_done;
@@ -390,6 +419,7 @@ struct PagedBars {
   int abort_flag;
   int is_last;
   int ticketed[2];       // the CTA's parts whose arrival has been counted
+  PagedCut cut[2];
   PagedItem item[kItemRing];
   PagedSetup setup;
 };
@@ -436,97 +466,113 @@ __device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
 // Counts a part's arrival; true for the item's last.  The word holds the
 // call's number and the parts so far; with another number in it (a new
 // workspace, whatever it held) the count is 0, and the last arrival leaves 0.
-__device__ __forceinline__ bool paged_ticket(const PagedParams &p, int cta0, int parts) {
-  unsigned long long *at = p.ticket + cta0;
+__device__ __forceinline__ bool paged_ticket(const PagedParams &p, PagedCut cut) {
+  unsigned long long *at = p.ticket + cut.cta0;
   unsigned long long old = *reinterpret_cast<volatile unsigned long long *>(at);
   while (true) {
     const unsigned long long n = ((old >> 16) == p.call ? (old & 0xffffull) : 0ull) + 1;
-    const bool last = n == static_cast<unsigned long long>(parts);
+    const bool last = n == static_cast<unsigned long long>(cut.parts);
     const unsigned long long now = atomicCAS(at, old, last ? 0ull : (p.call << 16) | n);
     if (now == old) return last;
     old = now;
   }
 }
 
+// A slot of the workspace: [D / 4][kPagedRows] float4, so that the threads of a
+// warp, which hold a row each, write and read neighbours.
+__device__ __forceinline__ float4 *paged_slot(const PagedParams &p, int D, int slot) {
+  return reinterpret_cast<float4 *>(p.ws_o) + static_cast<size_t>(slot) * kPagedRows * (D / 4);
+}
+
+// 16 results of one row, `c` its first column; 32-byte stores where every row
+// of the output is aligned for them.
+template <int DT>
+__device__ __forceinline__ void paged_store16(const PagedParams &p, uint8_t *orow, int c,
+                                              const float (&o)[16]) {
+  uint32_t w[8];
+#pragma unroll
+  for (int v = 0; v < 8; ++v) w[v] = pack2<DT>(o[2 * v], o[2 * v + 1]);
+  if (p.out_wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(orow + 2 * c),
+                 "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]),
+                 "r"(w[7])
+                 : "memory");
+  } else {
+    *reinterpret_cast<uint4 *>(orow + 2 * c) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4 *>(orow + 2 * c + 16) = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
 // Joins the parts of a cut item: m = max_i m_i, w_i = 2^(m_i - m),
-// O = sum_i w_i O_i / sum_i w_i l_i, lse = (m + log2 l) ln 2, in the order of
-// the parts, so that the result does not depend on which came last.  Part i
-// lies in slot 1 of CTA cta0 (i = 0) or slot 0 of CTA cta0 + i.  A warp joins
-// kRows rows at a time, lane / kRows takes a part's (m, l), and the rows' parts
-// are loaded together: the time is that of the loads' latency.
+// O = sum_i w_i O_i / sum_i w_i l_i, lse = (m + log2 l) ln 2, in a fixed order
+// of the parts, so that the result does not depend on which came last.  Part
+// i lies in slot 1 of CTA cta0 (i = 0) or slot 0 of CTA cta0 + i.  A warp takes
+// 32 rows and 16 columns at a time; fewer rows leave lanes that share a row's
+// parts among them (a decoding item cut over many CTAs).
 template <int D, int DT>
-__device__ __forceinline__ void paged_merge(const PagedParams &p, const PagedItem &t, int warp,
-                                            int warps) {
-  constexpr int kRows = 8, kLanes = 32 / kRows;
+__device__ __forceinline__ void paged_merge(const PagedParams &p, const PagedItem &t, PagedCut cut,
+                                            int warp, int warps) {
   const int lane = threadIdx.x & 31;
-  const int rows0 = t.nt0 * p.group, rows = rows0 + max(t.nt1, 0) * p.group;
-  auto place = [&](int k) {   // row k of the item in a slot
-    return static_cast<size_t>(k >= rows0 ? kBM + k - rows0 : k);
-  };
-  auto slot_of = [&](int i) {
-    return static_cast<size_t>(2 * (t.cta0 + i) + (i == 0 ? 1 : 0)) * kPagedRows;
-  };
-  for (int k0 = warp * kRows; k0 < rows; k0 += warps * kRows) {
-    // (rows behind the last one repeat it: their lanes only load)
-    const int mine = min(k0 + lane / kLanes, rows - 1);
+  const int rows0 = t.nt0 * p.group, rows1 = max(t.nt1, 0) * p.group;
+  const int n0 = (rows0 + 31) / 32, nb = n0 + (rows1 + 31) / 32;   // blocks of 32 rows
+  int R = 32;                                     // rows of a block, lanes / R share a row
+  if (nb == 1)
+    while (R / 2 >= rows0) R /= 2;
+  const int share = 32 / R, mine = lane / R;
+  auto slot_of = [&](int i) { return 2 * (cut.cta0 + i) + (i == 0 ? 1 : 0); };
+  for (int unit = warp; unit < nb * (D / 16); unit += warps) {
+    const int rb = unit % nb, c = unit / nb * 16;
+    const int tile = rb >= n0 ? 1 : 0;
+    const int rr = (rb - tile * n0) * 32 + lane % R;   // row within the tile
+    const bool valid = rr < (tile ? rows1 : rows0);    // (other rows were not written)
+    const size_t row = static_cast<size_t>(tile * kBM + rr);
     float m = -INFINITY;
-    for (int i = lane % kLanes; i < t.parts; i += kLanes)
-      m = fmaxf(m, __ldcg(&p.ws_ml[slot_of(i) + place(mine)]).x);
-#pragma unroll
-    for (int d = kLanes / 2; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    if (valid)
+      for (int i = mine; i < cut.parts; i += share)
+        m = fmaxf(m, __ldcg(&p.ws_ml[static_cast<size_t>(slot_of(i)) * kPagedRows + row]).x);
+    for (int d = R; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
     const float m_sub = m == -INFINITY ? 0.0f : m;
-    float4 acc[kRows];
+    float acc[16], l = 0.0f;
 #pragma unroll
-    for (int e = 0; e < kRows; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.0f;
-    for (int i0 = 0; i0 < t.parts; i0 += kLanes) {
-      // the weights of the next kLanes parts of the lane's row
-      const int i = i0 + lane % kLanes;
-      float w = 0.0f, wl = 0.0f;
-      if (i < t.parts) {
-        const float2 ml = __ldcg(&p.ws_ml[slot_of(i) + place(mine)]);
-        w = ex2(ml.x - m_sub);     // a part without a visible key: 0
-        wl = w * ml.y;
-      }
+    for (int v = 0; v < 16; ++v) acc[v] = 0.0f;
+    if (valid) {
 #pragma unroll 2
-      for (int j = 0; j < kLanes && i0 + j < t.parts; ++j) {
-        l += __shfl_sync(0xffffffffu, wl, (lane & ~(kLanes - 1)) + j);
-        float4 o[kRows];
+      for (int i = mine; i < cut.parts; i += share) {
+        const float2 ml = __ldcg(&p.ws_ml[static_cast<size_t>(slot_of(i)) * kPagedRows + row]);
+        const float4 *o = paged_slot(p, D, slot_of(i)) + static_cast<size_t>(c / 4) * kPagedRows + row;
+        float4 x[4];
 #pragma unroll
-        for (int e = 0; e < kRows; ++e)
-          if (lane * 4 < D)
-            o[e] = __ldcg(reinterpret_cast<const float4 *>(
-                              p.ws_o + (slot_of(i0 + j) + place(min(k0 + e, rows - 1))) * D) + lane);
+        for (int v = 0; v < 4; ++v) x[v] = __ldcg(o + v * kPagedRows);
+        const float w = ex2(ml.x - m_sub);   // a part without a visible key: 0
+        l += w * ml.y;
 #pragma unroll
-        for (int e = 0; e < kRows; ++e) {
-          const float we = __shfl_sync(0xffffffffu, w, e * kLanes + j);
-          acc[e].x += we * o[e].x;
-          acc[e].y += we * o[e].y;
-          acc[e].z += we * o[e].z;
-          acc[e].w += we * o[e].w;
+        for (int v = 0; v < 4; ++v) {
+          acc[4 * v] += w * x[v].x;
+          acc[4 * v + 1] += w * x[v].y;
+          acc[4 * v + 2] += w * x[v].z;
+          acc[4 * v + 3] += w * x[v].w;
         }
       }
     }
+    __syncwarp();
+    for (int d = R; d < 32; d <<= 1) {
+      l += __shfl_xor_sync(0xffffffffu, l, d);
 #pragma unroll
-    for (int e = 0; e < kRows; ++e) {
-      const int k = k0 + e;
-      const float le = __shfl_sync(0xffffffffu, l, e * kLanes);
-      const float me = __shfl_sync(0xffffffffu, m, e * kLanes);
-      if (k < rows) {
-        const int tile = k >= rows0 ? 1 : 0, rr = k - tile * rows0;
-        const float inv = le > 0.0f ? 1.0f / le : 0.0f;
-        const int tok = t.tok0 + tile * p.tile_q + rr / p.group;
-        const int head = t.h * p.group + rr % p.group;
-        if (lane * 4 < D)
-          *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.out) +
-                                     2 * (static_cast<long long>(tok) * p.out_st +
-                                          static_cast<long long>(head) * p.out_sh + 4 * lane)) =
-              make_uint2(pack2<DT>(acc[e].x * inv, acc[e].y * inv),
-                         pack2<DT>(acc[e].z * inv, acc[e].w * inv));
-        if (lane == 0 && p.lse != nullptr)
-          p.lse[static_cast<size_t>(tok) * p.H + head] =
-              le > 0.0f ? (me + __log2f(le)) * 0.6931471805599453f : -INFINITY;
-      }
+      for (int v = 0; v < 16; ++v) acc[v] += __shfl_xor_sync(0xffffffffu, acc[v], d);
+    }
+    if (valid && mine == 0) {
+      const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+      const int tok = t.tok0 + tile * p.tile_q + rr / p.group, head = t.h * p.group + rr % p.group;
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[v] *= inv;
+      paged_store16<DT>(p,
+                        static_cast<uint8_t *>(p.out) +
+                            2 * (static_cast<long long>(tok) * p.out_st +
+                                 static_cast<long long>(head) * p.out_sh),
+                        c, acc);
+      if (c == 0 && p.lse != nullptr)
+        p.lse[static_cast<size_t>(tok) * p.H + head] =
+            l > 0.0f ? (m + __log2f(l)) * 0.6931471805599453f : -INFINITY;
     }
   }
 }
@@ -577,6 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&bars->empty[s]), 1);
     }
     mbar_init(smem_u32(&bars->v_ragged), 1);
+    for (int s = 0; s < 2; ++s) mbar_init(smem_u32(&bars->cut_full[s]), 1);
     mbar_init(smem_u32(&bars->part_done), 8);
     mbar_init(smem_u32(&bars->part_last), 1);
     mbar_init(smem_u32(&bars->mma_done), 1);
@@ -597,6 +644,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   PagedCuts cuts;
   paged_find_piece(p, bars->setup, cuts);
+  __syncthreads();
+  PagedWalk walk;                     // (of the scheduling warp)
+  if (warp == kLoadWarpV) {           // its end, while that warp finds the start
+    long long end = cuts.at(blockIdx.x + 1);
+    walk.locate(p, bars->setup, 1, end);
+    if (lane == 0) bars->setup.end = end;
+  } else if (warp == kSchedWarp) {
+    walk.u = cuts.at(blockIdx.x);
+    walk.locate(p, bars->setup, 0, walk.u);
+  }
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
@@ -621,13 +678,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     // =================================================== schedule and Q
     // Items are announced up to kItemRing ahead of their last reader, one
     // ahead of their Q: a tile with key blocks takes the next of two Q slots.
-    PagedWalk walk;
-    walk.start(p, bars->setup, cuts);
+    walk.end = bars->setup.end;
     PagedItem t, ahead;
     int nq = 0, k = 0;
     const uint64_t pol = policy_evict_first();
     auto announce = [&](PagedItem &it) -> bool {
-      const bool more = walk.next(p, cuts, it);
+      const bool more = walk.next(p, it);
       const int s = k % kItemRing;
       if (k >= kItemRing)
         ok = mbar_wait_warp(smem_u32(&bars->item_empty[s]), (k / kItemRing - 1) & 1, abort_flag);
@@ -635,6 +691,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) {
         bars->item[s] = it;
         mbar_arrive(smem_u32(&bars->item_full[s]));
+        if (more && it.slot >= 0) {   // (read when the part is finished)
+          bars->cut[it.slot] = walk.cut_of(cuts);
+          mbar_arrive(smem_u32(&bars->cut_full[it.slot]));
+        }
       }
       __syncwarp();
       ++k;
@@ -1176,57 +1236,52 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (busy) {
         const float inv = t.slot >= 0 ? 1.0f : (l > 0.0f ? 1.0f / l : 0.0f);
         const int tok = t.tok0 + tile * p.tile_q + r_tok, head = t.h * p.group + r_head;
-        const size_t wrow =
-            static_cast<size_t>(2 * blockIdx.x + max(t.slot, 0)) * kPagedRows + tile * kBM + r;
         uint8_t *orow = static_cast<uint8_t *>(p.out) +
                         2 * (static_cast<long long>(tok) * p.out_st +
                              static_cast<long long>(head) * p.out_sh);
-        float *wo = p.ws_o + wrow * D;
+        const int slot = 2 * blockIdx.x + max(t.slot, 0), srow = tile * kBM + r;
+        float4 *wo = paged_slot(p, D, slot) + srow;
         const uint32_t from = single ? tO0 : tO;
         const float sa = wa * inv, sb = wb * inv;
 #pragma unroll 1
         for (int c = single ? 16 * u : 0; c < D; c += single ? 32 : 16) {
-          uint32_t o[16];
+          float o[16];
           if (none) {
 #pragma unroll
-            for (int v = 0; v < 16; ++v) o[v] = 0u;
+            for (int v = 0; v < 16; ++v) o[v] = 0.0f;
           } else {
-            tmem_ld_x16(from + c, o);
+            uint32_t x0[16];
+            tmem_ld_x16(from + c, x0);
             if (two) {
-              uint32_t o1[16];
-              tmem_ld_x16(from + D + c, o1);
+              uint32_t x1[16];
+              tmem_ld_x16(from + D + c, x1);
               tmem_wait_ld();
-              reg_dep(o);
-              reg_dep(o1);
+              reg_dep(x0);
+              reg_dep(x1);
 #pragma unroll
               for (int v = 0; v < 16; ++v)
-                o[v] = __float_as_uint(sa * __uint_as_float(o[v]) + sb * __uint_as_float(o1[v]));
+                o[v] = sa * __uint_as_float(x0[v]) + sb * __uint_as_float(x1[v]);
             } else {
               tmem_wait_ld();
-              reg_dep(o);
+              reg_dep(x0);
 #pragma unroll
-              for (int v = 0; v < 16; ++v) o[v] = __float_as_uint(sa * __uint_as_float(o[v]));
+              for (int v = 0; v < 16; ++v) o[v] = sa * __uint_as_float(x0[v]);
             }
           }
           if (valid && t.slot >= 0) {
 #pragma unroll
             for (int v = 0; v < 4; ++v)
-              *reinterpret_cast<float4 *>(wo + c + 4 * v) =
-                  make_float4(__uint_as_float(o[4 * v]), __uint_as_float(o[4 * v + 1]),
-                              __uint_as_float(o[4 * v + 2]), __uint_as_float(o[4 * v + 3]));
+              wo[(c / 4 + v) * kPagedRows] =
+                  make_float4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
           } else if (valid) {
-            uint32_t w[8];
-#pragma unroll
-            for (int v = 0; v < 8; ++v)
-              w[v] = pack2<DT>(__uint_as_float(o[2 * v]), __uint_as_float(o[2 * v + 1]));
-            *reinterpret_cast<uint4 *>(orow + 2 * c) = make_uint4(w[0], w[1], w[2], w[3]);
-            *reinterpret_cast<uint4 *>(orow + 2 * c + 16) = make_uint4(w[4], w[5], w[6], w[7]);
+            paged_store16<DT>(p, orow, c, o);
           }
           __syncwarp();   // the next chunk's load is warp-collective
         }
         if (valid && !(single && u == 1)) {
           if (t.slot >= 0)
-            p.ws_ml[wrow] = make_float2(l > 0.0f ? m_use : -INFINITY, l);
+            p.ws_ml[static_cast<size_t>(slot) * kPagedRows + srow] =
+                make_float2(l > 0.0f ? m_use : -INFINITY, l);
           else if (p.lse != nullptr)
             p.lse[static_cast<size_t>(tok) * p.H + head] =
                 l > 0.0f ? (m_use + __log2f(l)) * 0.6931471805599453f : -INFINITY;
@@ -1249,10 +1304,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         __threadfence();
         arrive(&bars->part_done);
         if (tid == 0) {
-          ok = mbar_wait(smem_u32(&bars->part_done), n_part & 1, abort_flag);
+          ok = mbar_wait(smem_u32(&bars->part_done), n_part & 1, abort_flag) &&
+               mbar_wait(smem_u32(&bars->cut_full[t.slot]), 0, abort_flag);
           if (ok) {
             __threadfence();
-            bars->is_last = paged_ticket(p, t.cta0, t.parts);
+            bars->is_last = paged_ticket(p, bars->cut[t.slot]);
             bars->ticketed[t.slot] = 1;
             __threadfence();
             mbar_arrive(smem_u32(&bars->part_last));
@@ -1265,7 +1321,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++n_part;
         if (bars->is_last) {
           __threadfence();
-          paged_merge<D, DT>(p, t, warp, 8);
+          paged_merge<D, DT>(p, t, bars->cut[t.slot], warp, 8);
         }
         // (is_last is written again only after all eight warps have arrived
         // for the next part)
@@ -1278,11 +1334,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (*abort_flag && warp == kSchedWarp) {
     // every part is counted, so that the tickets end at 0 for the next call
-    PagedWalk walk;
     PagedItem t;
     walk.start(p, bars->setup, cuts);
-    while (walk.next(p, cuts, t))
-      if (t.slot >= 0 && lane == 0 && !bars->ticketed[t.slot]) paged_ticket(p, t.cta0, t.parts);
+    while (walk.next(p, t))
+      if (t.slot >= 0 && lane == 0 && !bars->ticketed[t.slot]) paged_ticket(p, walk.cut_of(cuts));
   }
   if (warp == kMmaWarp) {
     tc_fence_after_sync();
