@@ -9,9 +9,10 @@ eager fallback: if libfa.so cannot be loaded, every call raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import math
 import os
-import struct
 import threading
 from typing import NamedTuple
 
@@ -118,7 +119,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.fa_bwd_ex.restype = i
         lib.fa_bwd_workspace_bytes.argtypes = [i, i, i, i]
         lib.fa_bwd_workspace_bytes.restype = ctypes.c_size_t
-        sz, pa = ctypes.c_size_t, ctypes.c_void_p   # (a FaRopeArgs by reference, or its bytes)
+        sz, pa = ctypes.c_size_t, ctypes.POINTER(FaRopeArgs)
         lib.fa_paged_plan.argtypes = [vp, vp, vp, ll, vp, i, i, i, i, i, vp, vp, vp, vp, vp, vp]
         lib.fa_paged_plan.restype = i
         lib.fa_qk_norm_rope.argtypes = [pa, vp]
@@ -653,9 +654,36 @@ def flash_fwd_host(q, k, v, scale=None, causal=False, window_left=-1, window_rig
 
 
 # ------------------------------------------------------------ serving
-# (These run once or more per layer of a decoding step, where a call's host
-# time counts: checks compare without copies, outputs come from few
-# allocations, the argument block is packed at once.)
+# These run for every layer of a decoding step, where a call's host time
+# counts: their checks and allocations are compiled (csrc/fa_torch.cpp).
+EXT_PATH = os.path.join(PKG, "lib", "_fa_torch.so")
+_ext = None
+
+
+def _serving():
+    """The compiled torch binding of the serving entries (in-tree build)."""
+    global _ext
+    load()
+    with _lock:
+        if _ext is None:
+            import torch  # noqa: F401  (its libraries, before the module that needs them)
+            if not os.path.exists(EXT_PATH):
+                raise RuntimeError(
+                    f"_fa_torch.so not found at {EXT_PATH}; build it with "
+                    "`python -m exact_attention_113_b200.build`")
+            loader = importlib.machinery.ExtensionFileLoader("_fa_torch", EXT_PATH)
+            spec = importlib.util.spec_from_file_location("_fa_torch", EXT_PATH, loader=loader)
+            ext = importlib.util.module_from_spec(spec)
+            loader.exec_module(ext)
+            ext.set_error(FaError)
+            _ext = ext
+    return _ext
+
+
+def _handle(stream):
+    return None if stream is None else stream.cuda_stream
+
+
 class PagedPlan(NamedTuple):
     """What paged_plan returns: device tensors of one serving step."""
     cu_q: "object"        # int32 [B + 1]
@@ -663,69 +691,6 @@ class PagedPlan(NamedTuple):
     positions: "object"   # int32 [num_tokens]
     slots: "object"       # int64 [num_tokens]
     counts: "object"      # int32 [3]: new tokens, pages taken, tokens without a slot
-
-
-def _call(dev, stream, where, fn, *args):
-    """fn(*args, stream) with device `dev` current; raises on a status."""
-    import torch
-
-    if stream is None:
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        handle = raw(dev) if raw is not None else torch.cuda.current_stream(dev).cuda_stream
-    else:
-        handle = stream.cuda_stream
-    if torch.cuda.current_device() == dev:
-        st = fn(*args, handle)
-    else:
-        with torch.cuda.device(dev):
-            st = fn(*args, handle)
-    if st != FA_OK:
-        raise FaError(st, where)
-
-
-def _on_device(dev, names, *tensors):
-    """Every tensor (None: not given) on CUDA device `dev`."""
-    for name, t in zip(names, tensors):
-        if t is not None and (dev < 0 or t.get_device() != dev):
-            raise ValueError(f"{name} must be a CUDA tensor on the same device as the others")
-
-
-def _vector(name, t, dtype, n):
-    if t.dtype != dtype or t.shape != (n,) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} vector of {n}")
-
-
-def _16bit(q):
-    import torch
-    if q.dtype == torch.float16:
-        return FA_F16
-    if q.dtype == torch.bfloat16:
-        return FA_BF16
-    raise TypeError("dtype must be float16 or bfloat16")
-
-
-def _cache_layout(k_cache, v_cache, H_kv, D, dtype):
-    """(pages, page size, element strides) of caches [pages, page_size, H_kv, D]."""
-    shape = k_cache.shape
-    if len(shape) != 4 or v_cache.shape != shape or shape[2] != H_kv or shape[3] != D:
-        raise ValueError("k_cache, v_cache must be [pages, page_size, H_kv, D]")
-    if k_cache.dtype != dtype or v_cache.dtype != dtype:
-        raise TypeError("k_cache, v_cache must have q's dtype")
-    st = k_cache.stride()
-    if st != v_cache.stride() or st[3] != 1:
-        raise ValueError("k_cache, v_cache must have the same strides, contiguous along D")
-    return shape[0], shape[1], st[0], st[1], st[2]
-
-
-def _table_layout(block_table, B):
-    """(columns, row stride) of a block table [B, max_pages]."""
-    import torch
-
-    if block_table.dim() != 2 or block_table.dtype != torch.int32 or block_table.shape[0] != B \
-            or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
-        raise ValueError("block_table must be int32 [B, max_pages], contiguous along the pages")
-    n = block_table.shape[1]
-    return n, block_table.stride(0) if B > 1 else max(n, 1)
 
 
 def paged_plan(q_lens, ctx_lens, block_table, free_pages, page_size, num_tokens, out=None,
@@ -739,77 +704,9 @@ def paged_plan(q_lens, ctx_lens, block_table, free_pages, page_size, num_tokens,
     captured graph's padding, gets -1).  ``out``: a PagedPlan to write into;
     otherwise its tensors share one allocation.  Nothing is read back:
     counts[2] > 0 tells that pages ran out."""
-    import torch
-
-    if q_lens.dim() != 1 or free_pages.dim() != 1:
-        raise ValueError("q_lens and free_pages must be vectors")
-    B, T = q_lens.shape[0], int(num_tokens)
-    i32 = torch.int32
-    _vector("q_lens", q_lens, i32, B)
-    _vector("ctx_lens", ctx_lens, i32, B)
-    n_free = free_pages.shape[0]
-    _vector("free_pages", free_pages, i32, n_free)
-    max_pages, table_stride = _table_layout(block_table, B)
-    dev = q_lens.get_device()
-    _on_device(dev, ("q_lens", "ctx_lens", "block_table", "free_pages"), q_lens, ctx_lens,
-               block_table, free_pages)
-    if out is None:
-        if T < 0:
-            raise ValueError("num_tokens must be >= 0")
-        # slots first: 8-byte values at the start of the allocation
-        buf = q_lens.new_empty(2 * T + T + 2 * B + 4)
-        slots, positions, cu_q, kv_lens, counts = buf.split((2 * T, T, B + 1, B, 3))
-        out = PagedPlan(cu_q, kv_lens, positions, slots.view(torch.int64), counts)
-    else:
-        for name, dt, n in (("cu_q", i32, B + 1), ("kv_lens", i32, B), ("positions", i32, T),
-                            ("slots", torch.int64, T), ("counts", i32, 3)):
-            _vector(name, getattr(out, name), dt, n)
-        _on_device(dev, PagedPlan._fields, *out)
-    lib = _lib or load()
-    _call(dev, stream, "fa_paged_plan", lib.fa_paged_plan, q_lens.data_ptr(), ctx_lens.data_ptr(),
-          block_table.data_ptr(), table_stride, free_pages.data_ptr(), n_free, B, max_pages,
-          int(page_size), T, out.cu_q.data_ptr(), out.kv_lens.data_ptr(),
-          out.positions.data_ptr(), out.slots.data_ptr(), out.counts.data_ptr())
-    return out
-
-
-def _rows(name, t, shape, dtype):
-    """fa_rows of a [T, H, D] or [B, L, H, D] tensor of the given shape, as a tuple."""
-    s = t.stride()
-    if t.shape != shape or t.dtype != dtype or s[-1] != 1:
-        raise ValueError(f"{name} must be {tuple(shape)}, {dtype}, contiguous along D")
-    return t.data_ptr(), (s[0] if len(s) == 4 else 0), s[-3], s[-2]
-
-
-_NO_ROWS = (0, 0, 0, 0)
-_NO_CACHE = (0, 0, 0, 0, 0, 0)
-_PACK_ROPE = struct.Struct("@32q12if4x")   # FaRopeArgs
-
-
-def _rope_common(q, k, q_weight, k_weight, cos_sin, positions):
-    """Checks shared by both directions: (dims, pointers) of fa_rope_args."""
-    import torch
-
-    qs, ks = q.shape, k.shape
-    if len(qs) not in (3, 4) or len(ks) != len(qs) or ks[:-2] != qs[:-2] or ks[-1] != qs[-1]:
-        raise ValueError("q, k must be [T, H, D] and [T, H_kv, D], or [B, L, H, D] and "
-                         "[B, L, H_kv, D]")
-    dtype, D = _16bit(q), qs[-1]
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _vector(name, w, q.dtype, D)
-    if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32 or not cos_sin.is_contiguous():
-        raise ValueError("cos_sin must be a contiguous float32 [max_pos, rot_dim]")
-    wide = positions.dtype == torch.int64
-    if positions.shape != qs[:-2] or not (wide or positions.dtype == torch.int32):
-        raise ValueError("positions must be int32 or int64 of q's token axes")
-    ps = positions.stride()
-    max_pos, rot = cos_sin.shape
-    ptrs = (0 if q_weight is None else q_weight.data_ptr(),
-            0 if k_weight is None else k_weight.data_ptr(), cos_sin.data_ptr(),
-            positions.data_ptr(), ps[0] if len(ps) == 2 else 0, ps[-1])
-    dims = (int(wide), qs[0] if len(qs) == 4 else 1, qs[-3], qs[-2], ks[-2], D, rot, max_pos)
-    return dtype, dims, ptrs
+    r = (_ext or _serving()).paged_plan(q_lens, ctx_lens, block_table, free_pages, page_size,
+                                        num_tokens, out, _handle(stream))
+    return PagedPlan._make(r) if out is None else out
 
 
 def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps=1e-6, interleaved=False,
@@ -831,34 +728,9 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps=1e-6, interle
     k_cache, v_cache [pages, page_size, H_kv, D] (strides free), v and slots
     (int64, one per token; negative: not written) k_out is only written if
     given.  Returns (q_out, k_out)."""
-    import torch
-
-    dtype, dims, ptrs = _rope_common(q, k, q_weight, k_weight, cos_sin, positions)
-    rows_v, cache, pages, page_size = _NO_ROWS, _NO_CACHE, 0, 0
-    cached = k_cache is not None or v_cache is not None
-    if cached:
-        if k_cache is None or v_cache is None or v is None or slots is None:
-            raise ValueError("a cache needs k_cache, v_cache, v and slots")
-        pages, page_size, sp, st, sh = _cache_layout(k_cache, v_cache, dims[4], dims[5], q.dtype)
-        rows_v = _rows("v", v, k.shape, q.dtype)
-        if slots.dtype != torch.int64 or slots.numel() != dims[1] * dims[2] \
-                or not slots.is_contiguous():
-            raise ValueError("slots must be contiguous int64, one per token")
-        cache = (k_cache.data_ptr(), v_cache.data_ptr(), sp, st, sh, slots.data_ptr())
-    dev = q.get_device()
-    _on_device(dev, ("q", "k", "q_weight", "k_weight", "cos_sin", "positions", "q_out", "k_out", "v",
-                     "k_cache", "v_cache", "slots"), q, k, q_weight, k_weight, cos_sin, positions,
-               q_out, k_out, v, k_cache, v_cache, slots)
-    if q_out is None:
-        q_out = q.new_empty(q.shape)
-    if k_out is None and not cached:
-        k_out = q.new_empty(k.shape)
-    rows_ko = _NO_ROWS if k_out is None else _rows("k_out", k_out, k.shape, q.dtype)
-    args = _PACK_ROPE.pack(*_rows("q", q, q.shape, q.dtype), *_rows("k", k, k.shape, q.dtype),
-                           *rows_v, *_rows("q_out", q_out, q.shape, q.dtype), *rows_ko, *ptrs,
-                           *cache, pages, page_size, *dims, int(interleaved), dtype, eps)
-    _call(dev, stream, "fa_qk_norm_rope", (_lib or load()).fa_qk_norm_rope, args)
-    return q_out, k_out
+    return (_ext or _serving()).qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps,
+                                             interleaved, q_out, k_out, v, k_cache, v_cache, slots,
+                                             _handle(stream))
 
 
 def qk_norm_rope_bwd(q, k, q_weight, k_weight, cos_sin, positions, dq_out, dk_out, eps=1e-6,
@@ -868,37 +740,9 @@ def qk_norm_rope_bwd(q, k, q_weight, k_weight, cos_sin, positions, dq_out, dk_ou
     float32 (None without a weight).  dq, dk: like q, k, any strides, allocated
     contiguous if None; dq may be dq_out itself.  The workspace is allocated
     here unless given (a uint8 CUDA tensor, 256-byte aligned)."""
-    import torch
-
-    dtype, dims, ptrs = _rope_common(q, k, q_weight, k_weight, cos_sin, positions)
-    dev = q.get_device()
-    _on_device(dev, ("q", "k", "q_weight", "k_weight", "cos_sin", "positions", "dq_out", "dk_out",
-                     "dq", "dk", "workspace"), q, k, q_weight, k_weight, cos_sin, positions, dq_out,
-               dk_out, dq, dk, workspace)
-    if dq is None:
-        dq = q.new_empty(q.shape)
-    if dk is None:
-        dk = q.new_empty(k.shape)
-    args = _PACK_ROPE.pack(*_rows("q", q, q.shape, q.dtype), *_rows("k", k, k.shape, q.dtype),
-                           *_NO_ROWS, *_rows("dq_out", dq_out, q.shape, q.dtype),
-                           *_rows("dk_out", dk_out, k.shape, q.dtype), *ptrs, *_NO_CACHE, 0, 0,
-                           *dims, int(interleaved), dtype, eps)
-    rq, rk = FaRows(*_rows("dq", dq, q.shape, q.dtype)), FaRows(*_rows("dk", dk, k.shape, q.dtype))
-    D = dims[5]
-    dwq = q.new_empty(D, dtype=torch.float32) if q_weight is not None else None
-    dwk = q.new_empty(D, dtype=torch.float32) if k_weight is not None else None
-    lib = _lib or load()
-
-    def run(handle):
-        ws = workspace
-        if ws is None:   # (sized for the current device)
-            ws = q.new_empty(max(lib.fa_qk_norm_rope_bwd_workspace_bytes(D), 1), dtype=torch.uint8)
-        return lib.fa_qk_norm_rope_bwd(args, rq, rk, None if dwq is None else dwq.data_ptr(),
-                                       None if dwk is None else dwk.data_ptr(), ws.data_ptr(),
-                                       ws.numel(), handle)
-
-    _call(dev, stream, "fa_qk_norm_rope_bwd", run)
-    return dq, dk, dwq, dwk
+    return (_ext or _serving()).qk_norm_rope_bwd(q, k, q_weight, k_weight, cos_sin, positions,
+                                                 dq_out, dk_out, eps, interleaved, dq, dk,
+                                                 workspace, _handle(stream))
 
 
 def flash_fwd_paged(q, k_cache, v_cache, block_table, cu_q, kv_lens, scale=None, causal=True,
@@ -916,51 +760,6 @@ def flash_fwd_paged(q, k_cache, v_cache, block_table, cu_q, kv_lens, scale=None,
     uint8 CUDA tensor of fa_paged_workspace_bytes(D), 256-byte aligned).
     Returns (out [total_q, H, D], lse float32 [total_q, H] or None); rows no
     request owns are not written."""
-    import torch
-
-    qst = q.stride()
-    if len(qst) != 3 or qst[2] != 1:
-        raise ValueError("q must be [total_q, H, D], contiguous along D")
-    T, H, D = q.shape
-    dtype = _16bit(q)
-    if k_cache.dim() != 4 or kv_lens.dim() != 1:
-        raise ValueError("k_cache, v_cache must be [pages, page_size, H_kv, D], kv_lens a vector")
-    H_kv = k_cache.shape[2]
-    pages, page_size, sp, st, sh = _cache_layout(k_cache, v_cache, H_kv, D, q.dtype)
-    B = kv_lens.shape[0]
-    _vector("kv_lens", kv_lens, torch.int32, B)
-    _vector("cu_q", cu_q, torch.int32, B + 1)
-    max_pages, table_stride = _table_layout(block_table, B)
-    dev = q.get_device()
-    _on_device(dev, ("q", "k_cache", "v_cache", "block_table", "cu_q", "kv_lens", "out", "lse",
-                     "workspace"), q, k_cache, v_cache, block_table, cu_q, kv_lens, out, lse,
-               workspace)
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
-    if out is None:
-        out = q.new_empty((T, H, D))
-    elif out.shape != q.shape or out.dtype != q.dtype or out.stride(2) != 1:
-        raise ValueError("out must be like q, contiguous along D")
-    if not return_lse:
-        lse = None
-    elif lse is None:
-        lse = q.new_empty((T, H), dtype=torch.float32)
-    elif lse.shape != (T, H) or lse.dtype != torch.float32 or not lse.is_contiguous():
-        raise ValueError("lse must be a contiguous float32 [total_q, H]")
-    ost = out.stride()
-    lib = _lib or load()
-
-    def run(handle):
-        ws = workspace
-        if ws is None:   # (sized for the current device)
-            ws = q.new_empty(max(lib.fa_paged_workspace_bytes(D), 1), dtype=torch.uint8)
-        return lib.fa_fwd_paged(q.data_ptr(), qst[0], qst[1], k_cache.data_ptr(),
-                                v_cache.data_ptr(), sp, st, sh, block_table.data_ptr(),
-                                table_stride, cu_q.data_ptr(), kv_lens.data_ptr(), out.data_ptr(),
-                                ost[0], ost[1], None if lse is None else lse.data_ptr(), T, B, H,
-                                H_kv, D, pages, page_size, max_pages, scale, bool(causal),
-                                window_left, window_right, dtype, ws.data_ptr(), ws.numel(),
-                                handle)
-
-    _call(dev, stream, "fa_fwd_paged", run)
-    return out, lse
+    return (_ext or _serving()).flash_fwd_paged(q, k_cache, v_cache, block_table, cu_q, kv_lens,
+                                                scale, causal, window_left, window_right,
+                                                return_lse, out, lse, workspace, _handle(stream))

@@ -1,4 +1,5 @@
-"""Build libfa.so (the C ABI of include/fa.h) for sm_100a with nvcc.
+"""Build libfa.so (the C ABI of include/fa.h) for sm_100a with nvcc, and its
+compiled torch binding with g++.
 
 The library is built in-tree, at exact_attention_113_b200/lib/libfa.so, and
 links the CUDA runtime statically; it reaches the driver's tensor-map encoder
@@ -106,9 +107,44 @@ TESTHOOKS_PATH = os.path.join(LIB_DIR, "libfa_testhooks.so")
 TESTHOOKS_FLAGS = ["-DFA_TEST_HOOKS", "-DFA_WAIT_LIMIT_NS=10000000ull"]
 
 
+# The compiled torch binding of the serving entries: plain C++ against torch's
+# headers, linked to libfa.so beside it; torch's own libraries are in the
+# process before it is imported.
+BINDING_SOURCE = os.path.join(CSRC, "fa_torch.cpp")
+BINDING_PATH = os.path.join(LIB_DIR, "_fa_torch.so")
+
+
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    depends = [BINDING_SOURCE, os.path.join(INCLUDE, "fa.h")]
+    if not force and os.path.exists(BINDING_PATH) and \
+            all(os.path.getmtime(p) <= os.path.getmtime(BINDING_PATH) for p in depends):
+        return BINDING_PATH
+    import sysconfig
+    import torch
+    from torch.utils import cpp_extension
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    tmp = BINDING_PATH + f".tmp{os.getpid()}"
+    dirs = cpp_extension.include_paths() + [sysconfig.get_paths()["include"],
+                                            os.path.join(cuda, "include"), INCLUDE]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-isystem{d}" for d in dirs), "-o", tmp, BINDING_SOURCE, f"-L{LIB_DIR}", "-l:libfa.so",
+           "-Wl,-rpath,$ORIGIN", *(f"-L{d}" for d in cpp_extension.library_paths()),
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0 or verbose:
+        sys.stderr.write(res.stdout + res.stderr)
+    if res.returncode != 0:
+        raise RuntimeError("g++ failed building _fa_torch.so")
+    os.replace(tmp, BINDING_PATH)
+    return BINDING_PATH
+
+
 def build(force: bool = False, verbose: bool = False, testhooks: bool = False) -> str:
     path = TESTHOOKS_PATH if testhooks else LIB_PATH
     if not force and not is_stale(path):
+        if not testhooks:
+            build_binding(verbose=verbose)
         return path
     os.makedirs(LIB_DIR, exist_ok=True)
     tmp = path + f".tmp{os.getpid()}"
@@ -140,6 +176,8 @@ def build(force: bool = False, verbose: bool = False, testhooks: bool = False) -
         for f in objects + [tmp]:
             if os.path.exists(f):
                 os.remove(f)
+    if not testhooks:
+        build_binding(force, verbose)
     return path
 
 
