@@ -44,7 +44,7 @@
 namespace fa {
 
 constexpr int kSchedWarp = 11;       // walks the work, loads Q
-constexpr int kPagedMinUnits = 3;    // cost a CTA gets at least
+constexpr int kPagedMinUnits = 2;    // cost a CTA gets at least
 constexpr int kPagedRows = 2 * kBM;  // rows of a work item
 constexpr int kItemRing = 3;         // items announced ahead
 
@@ -275,6 +275,7 @@ struct PagedItem {
   int first, kv_len, lo, hi; // position of the first token; key blocks of the part
   int lo0, hi0, lo1, hi1;    // ... of each tile
   int klo, khi, slot, b;     // keys some token of the item sees; -1: the whole item, else the part's slot
+  int once, pad[3];          // no other item reads these keys
 };
 // A cut item of this CTA (slot 0, slot 1): the CTA where it began, its parts.
 struct PagedCut {
@@ -357,6 +358,7 @@ struct PagedWalk {
     t.nt1 = min(p.tile_q, r.q_len - i0 - t.nt0);
     t.first = r.kv_len - r.q_len + i0;
     t.kv_len = r.kv_len;
+    t.once = r.q_len <= 2 * p.tile_q;
     int klo0, khi0, klo1 = 0, khi1 = -1;
     paged_keys(p, r, i0, t.nt0, klo0, khi0);
     t.klo = klo0;
@@ -737,7 +739,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const CUtensorMap *map = is_k ? &p.tm_k : &p.tm_v;
     const int per_block = kBN / p.box_rows;          // copies of rows per block
     const int in_mask = (1 << p.page_shift) - 1;
-    const uint64_t pol = policy_evict_last();
+    const uint64_t pol_keep = policy_evict_last(), pol_stream = policy_evict_first();
     PagedItem t;
     int q = 0;             // fills so far
     int ragged = 0;        // V: ragged blocks so far
@@ -794,6 +796,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait_clearing(smem_u32(&bars->item_full[k % kItemRing]), (k / kItemRing) & 1);
       if (!ok || !take(k, t)) break;
       const int *row = p.table + t.b * p.table_stride;
+      const uint64_t pol = t.once ? pol_stream : pol_keep;
       // page of this lane's rows of block j (-1: none), read one block ahead
       auto page_of = [&](int j) {
         const int pos = j * kBN + lane * p.box_rows;

@@ -8,12 +8,12 @@
 //   table[b, have + i] = free[first_b + i],  i < need - have;
 //   token t = cu_q[b] + i: position ctx_b + i, slot = page * P + position % P.
 //
-// One launch, bounded by its latency: every block scans all lengths, 256
-// requests at a time (two prefix sums), and then serves its own 1024 tokens
-// and its share of the new pages, so no block waits for another.  A token or
-// page finds its request by a search in the tile's prefix sums.  A new token's
-// page is taken from the free list directly, not from the table that another
-// block may be writing.
+// One launch, bounded by its latency: every block scans all lengths, 1024
+// requests at a time (two prefix sums, four requests a thread), and then serves
+// its own 1024 tokens and its share of the new pages, so no block waits for
+// another.  A token or page finds its request by a search in the tile's prefix
+// sums.  A new token's page is taken from the free list directly, not from the
+// table that another block may be writing.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -22,6 +22,7 @@ namespace fa {
 
 constexpr int kPlanThreads = 256;
 constexpr int kPlanTokens = 1024;   // tokens of a block
+constexpr int kPlanTile = 1024;     // requests scanned at a time
 
 struct PlanParams {
   const int *q_lens, *ctx_lens;
@@ -39,18 +40,23 @@ __device__ __forceinline__ int plan_sat(long long v) {
 }
 
 __global__ void __launch_bounds__(kPlanThreads) fa_plan_kernel(const PlanParams p) {
-  __shared__ long long tok_s[kPlanThreads];       // first token of each request of the tile
-  __shared__ long long page_s[kPlanThreads];      // first free-list entry
-  __shared__ int ctx_s[kPlanThreads];
-  __shared__ long long warp_t[kPlanThreads / 32], warp_p[kPlanThreads / 32];
-  __shared__ long long short_s[kPlanThreads / 32];
+  constexpr int kWarps = kPlanThreads / 32, kEach = kPlanTile / kPlanThreads;
+  __shared__ long long tok_s[kPlanTile];    // first token of each request of the tile
+  __shared__ long long page_s[kPlanTile];   // first free-list entry
+  __shared__ int ctx_s[kPlanTile];
+  __shared__ long long warp_t[kWarps], warp_p[kWarps], short_s[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int P = p.page_size;
   const long long t0 = static_cast<long long>(blockIdx.x) * kPlanTokens;
   const long long t1 = min(t0 + kPlanTokens, static_cast<long long>(p.num_tokens));
-  // the last request of the tile whose prefix sum is at most v
-  auto find = [](const long long *pre, long long v) {
-    int lo = 0, hi = kPlanThreads;
+  // pages of n tokens (n < 2^32: contexts and new tokens are ints)
+  auto pages_of = [&](long long n) {
+    return static_cast<int>(static_cast<unsigned>(n) / static_cast<unsigned>(P)) +
+           (static_cast<unsigned>(n) % static_cast<unsigned>(P) != 0);
+  };
+  // the last request of the tile (of n) whose prefix sum is at most v
+  auto find = [](const long long *pre, int n, long long v) {
+    int lo = 0, hi = n;
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
       if (pre[mid] <= v) lo = mid; else hi = mid;
@@ -59,18 +65,24 @@ __global__ void __launch_bounds__(kPlanThreads) fa_plan_kernel(const PlanParams 
   };
   long long tokens = 0, pages = 0;   // before the tile
   long long missing = 0;             // this thread's requests'
-  for (int base = 0, tile = 0; base < p.B; base += kPlanThreads, ++tile) {
-    const int b = base + tid;
-    int q = 0, ctx = 0;
-    if (b < p.B) {
-      q = max(p.q_lens[b], 0);
-      ctx = max(p.ctx_lens[b], 0);
+  for (int base = 0, tile = 0; base < p.B; base += kPlanTile, ++tile) {
+    const int n = min(kPlanTile, p.B - base);
+    int q[kEach], ctx[kEach], grown[kEach];
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const int i = tid * kEach + e;
+      q[e] = i < n ? max(p.q_lens[base + i], 0) : 0;
+      ctx[e] = i < n ? max(p.ctx_lens[base + i], 0) : 0;
     }
-    const long long kv = static_cast<long long>(ctx) + q;
-    const int have = static_cast<int>((static_cast<long long>(ctx) + P - 1) / P);
-    const int need = static_cast<int>(min((kv + P - 1) / P, static_cast<long long>(p.max_pages)));
-    const int grown = max(need - have, 0);
-    long long it = q, ip = grown;
+    long long it = 0, ip = 0;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      grown[e] = max(min(pages_of(static_cast<long long>(ctx[e]) + q[e]), p.max_pages) -
+                         pages_of(ctx[e]), 0);
+      it += q[e];
+      ip += grown[e];
+    }
+    const long long mine_t = it, mine_p = ip;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const long long a = __shfl_up_sync(0xffffffffu, it, d), c = __shfl_up_sync(0xffffffffu, ip, d);
@@ -79,15 +91,16 @@ __global__ void __launch_bounds__(kPlanThreads) fa_plan_kernel(const PlanParams 
         ip += c;
       }
     }
-    __syncthreads();   // the tile before has been read
+    if (base > 0) __syncthreads();   // the tile before has been read
     if (lane == 31) {
       warp_t[warp] = it;
       warp_p[warp] = ip;
     }
     __syncthreads();
     const long long pages0 = pages;
-    long long at = tokens + it - q, first = pages + ip - grown;
-    for (int w = 0; w < kPlanThreads / 32; ++w) {
+    long long at = tokens + it - mine_t, first = pages + ip - mine_p;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
       if (w < warp) {
         at += warp_t[w];
         first += warp_p[w];
@@ -95,36 +108,43 @@ __global__ void __launch_bounds__(kPlanThreads) fa_plan_kernel(const PlanParams 
       tokens += warp_t[w];
       pages += warp_p[w];
     }
-    tok_s[tid] = at;
-    page_s[tid] = first;
-    ctx_s[tid] = ctx;
-    if (b < p.B && tile % gridDim.x == blockIdx.x) {
-      p.cu_q[b] = plan_sat(at);
-      if (b == p.B - 1) p.cu_q[p.B] = plan_sat(at + q);
-      p.kv_lens[b] = plan_sat(kv);
-    }
-    if (blockIdx.x == 0) {
-      // new tokens behind the last page the request could get
-      const long long got = min(static_cast<long long>(grown), max(p.n_free - first, 0ll));
-      const long long room = (static_cast<long long>(min(have, p.max_pages)) + got) * P - ctx;
-      missing += q - min(static_cast<long long>(q), max(room, 0ll));
+    const bool writes = tile % gridDim.x == blockIdx.x;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const int i = tid * kEach + e;
+      tok_s[i] = at;
+      page_s[i] = first;
+      ctx_s[i] = ctx[e];
+      if (i < n && writes) {
+        p.cu_q[base + i] = plan_sat(at);
+        if (base + i == p.B - 1) p.cu_q[p.B] = plan_sat(at + q[e]);
+        p.kv_lens[base + i] = plan_sat(static_cast<long long>(ctx[e]) + q[e]);
+      }
+      if (blockIdx.x == 0) {
+        // new tokens behind the last page the request could get
+        const long long got = min(static_cast<long long>(grown[e]), max(p.n_free - first, 0ll));
+        const long long room =
+            (static_cast<long long>(min(pages_of(ctx[e]), p.max_pages)) + got) * P - ctx[e];
+        missing += q[e] - min(static_cast<long long>(q[e]), max(room, 0ll));
+      }
+      at += q[e];
+      first += grown[e];
     }
     __syncthreads();
     for (long long k = pages0 + static_cast<long long>(blockIdx.x) * kPlanThreads + tid; k < pages;
          k += static_cast<long long>(gridDim.x) * kPlanThreads) {
-      const int lo = find(page_s, k);
-      const long long old = (static_cast<long long>(ctx_s[lo]) + P - 1) / P;
-      p.table[(base + lo) * p.table_stride + old + k - page_s[lo]] =
+      const int lo = find(page_s, n, k);
+      p.table[(base + lo) * p.table_stride + pages_of(ctx_s[lo]) + k - page_s[lo]] =
           k < p.n_free ? p.free_pages[k] : -1;
     }
     for (long long t = max(t0, tok_s[0]) + tid; t < min(t1, tokens); t += kPlanThreads) {
-      const int lo = find(tok_s, t);
-      const long long pos = ctx_s[lo] + (t - tok_s[lo]);
-      const long long pg = pos / P;
-      const long long old = (static_cast<long long>(ctx_s[lo]) + P - 1) / P;
+      const int lo = find(tok_s, n, t);
+      const unsigned pos = static_cast<unsigned>(ctx_s[lo] + (t - tok_s[lo]));
+      const unsigned pg = pos / static_cast<unsigned>(P);
+      const int old = pages_of(ctx_s[lo]);
       int page = -1;
-      if (pg < p.max_pages) {
-        if (pg < old) {
+      if (pg < static_cast<unsigned>(p.max_pages)) {
+        if (static_cast<int>(pg) < old) {
           page = p.table[(base + lo) * p.table_stride + pg];
         } else {
           const long long f = page_s[lo] + pg - old;
@@ -132,7 +152,8 @@ __global__ void __launch_bounds__(kPlanThreads) fa_plan_kernel(const PlanParams 
         }
       }
       p.positions[t] = plan_sat(pos);
-      p.slots[t] = page < 0 ? -1 : static_cast<long long>(page) * P + pos % P;
+      p.slots[t] = page < 0 ? -1
+                            : static_cast<long long>(page) * P + (pos - pg * static_cast<unsigned>(P));
     }
   }
   for (long long t = max(t0, tokens) + tid; t < t1; t += kPlanThreads) {   // padding
@@ -145,7 +166,7 @@ __global__ void __launch_bounds__(kPlanThreads) fa_plan_kernel(const PlanParams 
     if (lane == 0) short_s[warp] = missing;
     __syncthreads();
     if (tid == 0) {
-      for (int w = 1; w < kPlanThreads / 32; ++w) missing += short_s[w];
+      for (int w = 1; w < kWarps; ++w) missing += short_s[w];
       p.counts[0] = plan_sat(tokens);
       p.counts[1] = plan_sat(min(pages, static_cast<long long>(p.n_free)));
       p.counts[2] = plan_sat(missing);

@@ -356,19 +356,24 @@ PyObject *qk_norm_rope_bwd(PyObject *, PyObject *const *a, Py_ssize_t na) {
   at::Tensor o[4];   // dq, dk, dq_weight, dk_weight
   if (dq) o[0] = *dq; else o[0] = empty(q->sizes(), q, type);
   if (dk) o[1] = *dk; else o[1] = empty(k->sizes(), q, type);
-  if (wq) o[2] = empty({r.D}, q, at::kFloat);
-  if (wk) o[3] = empty({r.D}, q, at::kFloat);
   const fa_rows rq = rows_of(&o[0], "dq", q->sizes(), type), rk = rows_of(&o[1], "dk", k->sizes(), type);
+  // the weight gradients (one allocation) and, unless given, the workspace
+  if (wq || wk) {
+    const at::Tensor both = empty({2ll * r.D}, q, at::kFloat);
+    if (wq) o[2] = part(both, at::kFloat, 0, r.D);
+    if (wk) o[3] = part(both, at::kFloat, r.D, r.D);
+  }
   at::Tensor own;
-  if (!ws) {
-    own = empty({static_cast<int64_t>(fa_qk_norm_rope_bwd_workspace_bytes(r.D)) + 1}, q, at::kByte);
+  if (!ws && (wq || wk)) {
+    own = empty({static_cast<int64_t>(fa_qk_norm_rope_bwd_workspace_bytes(r.D))}, q, at::kByte);
     ws = &own;
   }
   const cudaStream_t s = stream_of(a[13], dev.index);
   call("fa_qk_norm_rope_bwd", [&] {
     return fa_qk_norm_rope_bwd(&r, rq, rk, wq ? static_cast<float *>(o[2].data_ptr()) : nullptr,
                                wk ? static_cast<float *>(o[3].data_ptr()) : nullptr,
-                               ws->data_ptr(), static_cast<size_t>(ws->numel()) * ws->element_size(), s);
+                               ws ? ws->data_ptr() : nullptr,
+                               ws ? static_cast<size_t>(ws->numel()) * ws->element_size() : 0, s);
   });
   PyObject *res = PyTuple_New(4);
   for (int i = 0; res && i < 4; ++i) {
