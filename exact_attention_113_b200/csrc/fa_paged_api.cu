@@ -202,7 +202,9 @@ extern "C" int fa_fwd_paged(const void *q, long long q_stride_t, long long q_str
   const long long cd[4] = {D, page_size, H_kv, num_pages};
   const long long cs[4] = {1, cache_stride_token, cache_stride_head, cache_stride_page};
   const int cb[4] = {cols, p.box_rows, 1, 1};
-  if (!encode(&p.tm_q, q, dtype, 3, qd, qs, qb) || !encode(&p.tm_k, k_cache, dtype, 4, cd, cs, cb) ||
+  const int qb1[3] = {cols, p.group, 1};
+  if (!encode(&p.tm_q, q, dtype, 3, qd, qs, qb) || !encode(&p.tm_q1, q, dtype, 3, qd, qs, qb1) ||
+      !encode(&p.tm_k, k_cache, dtype, 4, cd, cs, cb) ||
       !encode(&p.tm_v, v_cache, dtype, 4, cd, cs, cb))
     return FA_ERR_CUDA;
   switch (D * 2 + dtype) {

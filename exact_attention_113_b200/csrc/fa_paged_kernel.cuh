@@ -50,6 +50,7 @@ constexpr int kItemRing = 3;         // items announced ahead
 
 struct PagedParams {
   CUtensorMap tm_q;   // (D, H, total_q), box (cols, G, TQ)
+  CUtensorMap tm_q1;  // the same, box (cols, G, 1)
   CUtensorMap tm_k;   // (D, P, H_kv, pages), box (cols, box_rows, 1, 1)
   CUtensorMap tm_v;
   const int *table;
@@ -636,14 +637,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tensormap(&p.tm_k);
     prefetch_tensormap(&p.tm_v);
   }
-  // tiles of fewer than 128 rows (a group that does not divide 128): the rows
-  // behind them are never copied, so they are set once
+  // Rows that no copy writes are zero: behind tiles of fewer than 128 rows (a
+  // group that does not divide 128), and behind a single token's, whose other
+  // 124 or so rows of products then switch next to nothing: with other
+  // requests' rows in them a decoding batch ran into the board's power limit
+  // (64 requests over 8k, for seconds: 370 us at 1.37 GHz, with zeros 327).
   const int q_rows = p.tile_q * p.group;
-  if (q_rows < kBM) {
-    for (int i = tid; i < 2 * G::kTileBytes / 16; i += kThreads)
-      reinterpret_cast<uint4 *>(smem + G::kOffQ)[i] = make_uint4(0, 0, 0, 0);
-    fence_proxy_async_smem();
-  }
+  for (int i = tid; i < 2 * G::kTileBytes / 16; i += kThreads)
+    reinterpret_cast<uint4 *>(smem + G::kOffQ)[i] = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
   PagedCuts cuts;
   paged_find_piece(p, bars->setup, cuts);
   __syncthreads();
@@ -702,17 +704,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++k;
       return more;
     };
-    auto load = [&](int h, int tok) {
+    int dirty = 0;   // slots whose rows behind the first token may not be zero
+    auto load = [&](int h, int tok, int n) {
       const int s = nq & 1;
       if (nq >= 2) ok = mbar_wait_warp(smem_u32(&bars->q_empty[s]), ((nq >> 1) - 1) & 1, abort_flag);
       if (!ok) return;
+      const bool one = n == 1;
+      if (!one) {
+        dirty |= 1 << s;
+      } else if (dirty & (1 << s)) {
+        dirty &= ~(1 << s);
+        constexpr int kUnits = G::kUnitsPerBoxRow;
+#pragma unroll 1
+        for (int bx = 0; bx < G::kNumBox; ++bx)
+#pragma unroll 4
+          for (int i = p.group * kUnits + lane; i < kBM * kUnits; i += 32)
+            reinterpret_cast<uint4 *>(smem + G::kOffQ + s * G::kTileBytes + bx * G::kBoxBytes)[i] =
+                make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
       const uint32_t bar = smem_u32(&bars->q_full[s]);
       if (elect_one()) {
-        mbar_arrive_expect_tx(bar, q_rows * G::kRowBytes);
+        mbar_arrive_expect_tx(bar, (one ? p.group : q_rows) * G::kRowBytes);
 #pragma unroll
         for (int bx = 0; bx < G::kNumBox; ++bx)
-          tma_load_3d(sQ + s * G::kTileBytes + bx * G::kBoxBytes, &p.tm_q, bar, bx * G::kBoxCols,
-                      h * p.group, tok, pol);
+          tma_load_3d(sQ + s * G::kTileBytes + bx * G::kBoxBytes, one ? &p.tm_q1 : &p.tm_q, bar,
+                      bx * G::kBoxCols, h * p.group, tok, pol);
       }
       __syncwarp();
       ++nq;
@@ -720,8 +738,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool more = announce(t);
     while (ok && more) {
       more = announce(ahead);
-      if (ok && t.hi0 > t.lo0) load(t.h, t.tok0);
-      if (ok && t.hi1 > t.lo1) load(t.h, t.tok0 + p.tile_q);
+      if (ok && t.hi0 > t.lo0) load(t.h, t.tok0, t.nt0);
+      if (ok && t.hi1 > t.lo1) load(t.h, t.tok0 + p.tile_q, t.nt1);
       t = ahead;
     }
     if (!ok)   // let the copies in flight land before the CTA exits
@@ -1072,6 +1090,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             arrive(&bars->s_free[u]);
             if (ns > 0) ok = mbar_wait_warp(smem_u32(&bars->pv_done[u]), (ns - 1) & 1, abort_flag);
             if (!ok) break;
+            if (n == 0) {   // zeros, for the power (beside S, P is what an earlier item left)
+              tc_fence_after_sync();
+              uint32_t z[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) z[i] = 0u;
+              store_p_half<DT>(tP, 0, z);
+              store_p_half<DT>(tP, 1, z);
+              tmem_wait_st();
+            }
           }
         } else {
           const bool full = k0 >= full_lo && k0 + kBN - 1 <= full_hi;
@@ -1119,10 +1146,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                                   fmaxf(sv[kBN - 2], sv[kBN - 1]));
             return m == -INFINITY ? -INFINITY : m * sl2;
           };
+          // minus the reference; rows that are none get zero weights
+          auto neg_ref = [&]() {
+            return !valid ? -INFINITY : (m_use == -INFINITY ? 0.0f : -m_use);
+          };
           // P of one half against the reference; the weights summed unrounded
           auto exp_half = [&](const float (&sv)[kBN], int half, uint32_t (&pk)[32]) {
-            const float m_sub = (m_use == -INFINITY) ? 0.0f : m_use;
-            const float2 negm = make_float2(-m_sub, -m_sub);
+            const float nm = neg_ref();
+            const float2 negm = make_float2(nm, nm);
 #pragma unroll
             for (int c = 0; c < kBN / 2; c += 2) {
               const float2 e =
@@ -1168,7 +1199,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (full && __all_sync(0xffffffffu, m_use != -INFINITY)) {
               float s[kBN];
               load_s(s);
-              const float2 negm = make_float2(-m_use, -m_use);
+              const float nm = neg_ref();
+              const float2 negm = make_float2(nm, nm);
               float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
               float2 lf[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
               uint32_t pk[2][32];
