@@ -15,20 +15,22 @@
 // hold whole pairs (8 values from each half, or 16 neighbours), so the rotation
 // needs no exchange and only the norm's sum crosses lanes.  Rows are copied to
 // shared memory some steps ahead.  All arithmetic is fp32; the result is
-// rounded once.  Measured: forward 0.90 of the HBM copy rate at B4 L8192 H48
-// D64 (137 us), gradient 0.78 at B2 L16384 H32/8 D128 (200 us).
+// rounded once.  Measured: forward 0.87 of the HBM copy rate at B4 L8192 H48
+// D64 (141 us), 0.70 with the cache at 8192 tokens (45 us); gradient 0.85 at B2
+// L16384 H32/8 D128 (183 us).
 #pragma once
 
 #include "sm100.cuh"
 
 namespace fa {
 
-// Stages and blocks per SM, measured on 8192 tokens (48 rows of D 128 each) and
-// on B4 L8192 H48 D64: 4 stages, 4 blocks 51 / 137 us; 5 blocks (fewer
-// registers) 53 / 142; 3 stages 51 / 141.  The gradient at B2 L16384 H32/8
-// D128: 3 stages, 4 blocks 200 us; 2 stages 208; 4 stages 210.
+// Stages and blocks per SM, measured on 8192 tokens (32 + 8 + 8 rows of D 128,
+// to the cache) and on B4 L8192 H48 D64: 3 stages, 4 blocks 45 / 141 us; 2
+// stages 54 / 178, 4 stages 45 / 150 (more shared memory, less L1); 3 blocks
+// 49 / 158, 5 blocks 47 / 152.  The gradient at B2 L16384 H32/8 D128: 3 stages,
+// 4 blocks 183 us; 2 stages 212; 4 stages 189.
 constexpr int kRopeThreads = 128;
-constexpr int kRopeStages = 4;        // rows a lane has in shared memory
+constexpr int kRopeStages = 3;        // rows a lane has in shared memory
 constexpr int kRopeBlocks = 4;        // resident per SM
 constexpr int kRopeBwdStages = 3;
 constexpr int kRopeBwdBlocks = 4;
@@ -58,9 +60,9 @@ struct RopeParams {
   RopeView dq, dk;        // written
   float *part;            // [blocks][D] partial weight gradients
   float *dwq, *dwk;       // [D]
-  int blocks_q, blocks_k;     // blocks of query rows, key rows (the rest: value rows)
-  int chunks_q, chunks_k;     // chunks of a token's rows
-  int per_q, per_k;           // steps of a chunk
+  int blocks_q, blocks_k;     // blocks of query rows, of key rows (the rest: value rows)
+  int chunks_q, chunks_k;     // chunks of a token's rows, and their steps (forward)
+  int per_q, per_k;
 };
 
 // This lane's place in a row of D values: two vectors of 8 and whether they
@@ -157,10 +159,12 @@ __device__ __forceinline__ float seg_sum(float v) {
   return v;
 }
 
-__device__ __forceinline__ long long rope_position(const RopeParams &p, int b, int l) {
-  const long long at = b * p.pos_sb + l * p.pos_sl;
-  return p.pos64 ? __ldg(static_cast<const long long *>(p.pos) + at)
-                 : static_cast<long long>(__ldg(static_cast<const int *>(p.pos) + at));
+__device__ __forceinline__ const void *rope_position(const RopeParams &p, int b, int l) {
+  return static_cast<const char *>(p.pos) + (b * p.pos_sb + l * p.pos_sl) * (p.pos64 ? 8 : 4);
+}
+// The position that copy8 brought.
+__device__ __forceinline__ long long rope_position_of(const RopeParams &p, const long long *at) {
+  return p.pos64 ? *at : static_cast<long long>(*reinterpret_cast<const int *>(at));
 }
 
 // The lane's cosines and sines (the first reading of a row of the table comes
@@ -183,6 +187,13 @@ __device__ __forceinline__ Row16 rope_weight(const void *weight, const RopeLane 
 
 __device__ __forceinline__ void st16(uint8_t *p, const uint4 &v) { *reinterpret_cast<uint4 *>(p) = v; }
 
+// 4 or 8 bytes, the same way.
+__device__ __forceinline__ void copy8(long long *dst, const void *src, bool wide) {
+  if (wide)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
 // 16 bytes into the lane's own place in shared memory, asynchronously; zeros
 // where !ok (nothing is read then).
 __device__ __forceinline__ void copy16(uint4 *dst, const uint8_t *src, bool ok) {
@@ -208,15 +219,15 @@ struct RopeWalk {
 
 // Every n-th chunk of at most `per` steps: the warps that run together work on
 // neighbouring tokens, whose rows of one head are neighbours in a
-// [B, H, L, D] output (the forward at B4 L8192 H48 D64: 139 us, in runs 162).
+// [B, H, L, D] output (the forward at B4 L8192 H48 D64: 141 us, in runs 162).
 struct RopeChunks : RopeWalk {
   unsigned item, items, n;
   int steps, chunks, per, end;
-  __device__ __forceinline__ void start(const RopeParams &p, bool is_q, unsigned me, unsigned warps,
-                                        int steps_) {
+  __device__ __forceinline__ void start(const RopeParams &p, unsigned me, unsigned warps, int steps_,
+                                        int chunks_, int per_) {
     steps = steps_;
-    chunks = is_q ? p.chunks_q : p.chunks_k;
-    per = is_q ? p.per_q : p.per_k;
+    chunks = chunks_;
+    per = per_;
     item = me;
     items = p.B * p.L * chunks;
     n = warps;
@@ -241,11 +252,11 @@ struct RopeChunks : RopeWalk {
 };
 
 // An equal run of steps for each warp, tokens in order: the fewest
-// instructions (the gradient at B2 L16384 H32/8 D128: 202 us, in chunks 230).
+// instructions (the gradient at B2 L16384 H32/8 D128: in chunks 15 % slower).
 struct RopeRun : RopeWalk {
   unsigned at, to;
   int steps;
-  __device__ __forceinline__ void start(const RopeParams &p, bool, unsigned me, unsigned warps,
+  __device__ __forceinline__ void start(const RopeParams &p, unsigned me, unsigned warps,
                                         int steps_) {
     steps = steps_;
     const unsigned total = p.B * p.L * steps, q = total / warps, rest = total % warps;
@@ -271,41 +282,65 @@ struct RopeRun : RopeWalk {
   }
 };
 
+// Where token (b, l) goes in a cache; false: nowhere.
+__device__ __forceinline__ bool rope_slot(const RopeParams &p, long long slot, long long &at) {
+  if (slot < 0 || slot >= p.n_slots) return false;
+  long long page, in_page;
+  if (p.n_slots <= 0x7fffffffll) {   // (a 32-bit division is a third of the cost)
+    page = static_cast<unsigned>(slot) / static_cast<unsigned>(p.page_size);
+    in_page = static_cast<unsigned>(slot) % static_cast<unsigned>(p.page_size);
+  } else {
+    page = slot / p.page_size;
+    in_page = slot % p.page_size;
+  }
+  at = page * p.c_sp + in_page * p.c_st;
+  return true;
+}
+
 // kSeg lanes a row: the smallest power of two >= D / 16.  Blocks are dealt to
-// the kinds of rows (query, key, and value rows, which only move to the cache)
-// in proportion, and a kind's chunks to its warps.  A lane has its next kRopeStages - 1 rows under way in shared memory, where no registers
-// wait for them and, as it reads only what it copied itself, no barrier either.
+// the kinds of rows (query, key, and value rows, which only move to the cache),
+// and a kind's chunks to its warps.  A lane has its next kRopeStages - 1 rows
+// under way in shared memory, where no registers wait for them and, as it
+// reads only what it copied itself, no barrier either; a token's position and
+// slot come the same way, with its first row.
 template <int kSeg, int DT, bool kInter>
 __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
     fa_rope_fwd_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kRowsWarp = 32 / kSeg, S = kRopeStages, kWarps = kRopeThreads / 32;
   __shared__ uint4 ring[kWarps][S][2][32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, s = lane % kSeg;
-  const int bid = blockIdx.x;
-  const bool is_q = bid < p.blocks_q, is_v = bid >= p.blocks_q + p.blocks_k;
-  const int blocks = is_q ? p.blocks_q : (is_v ? gridDim.x - p.blocks_q - p.blocks_k : p.blocks_k);
-  const unsigned me = (bid - (is_q ? 0 : (is_v ? p.blocks_q + p.blocks_k : p.blocks_q))) * kWarps + warp;
+  __shared__ long long meta[kWarps][S][2][32];   // position, slot
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, s = lane % kSeg, hl = lane / kSeg;
+  const int bid = blockIdx.x, qk = p.blocks_q + p.blocks_k;
+  const bool is_q = bid < p.blocks_q, is_v = bid >= qk;
+  const int first = is_q ? 0 : (is_v ? qk : p.blocks_q);
+  const int blocks = is_q ? p.blocks_q : (is_v ? gridDim.x - qk : p.blocks_k);
   const int H = is_q ? p.H : p.H_kv;
-  const int steps = (H + kRowsWarp - 1) / kRowsWarp;
   const RopeView in = is_q ? p.q : (is_v ? p.v : p.k), out = is_q ? p.qo : p.ko;
+  const bool cached = !is_q && p.kc, want = !is_v && out.ptr;
   RopeLane w = rope_lane(s, p.D, p.rot, kInter);
   if (is_v) {   // copied: neighbouring vectors, whatever the pairs are
     w.a = 16 * s;
     w.b = 16 * s + 8;
   }
-  const int ab = 2 * (w.b - w.a), hl = lane / kSeg;
+  const int ab = 2 * (w.b - w.a);
   const void *weight = is_v ? nullptr : (is_q ? p.wq : p.wk);
   Row16 g;
   if (w.on && weight) g = rope_weight<DT>(weight, w);
-
   RopeChunks fw, cw;
-  fw.start(p, is_q, me, blocks * kWarps, steps);
+  fw.start(p, (bid - first) * kWarps + warp, blocks * kWarps, (H + kRowsWarp - 1) / kRowsWarp,
+           is_q ? p.chunks_q : p.chunks_k, is_q ? p.per_q : p.per_k);
   cw = fw;
   const uint8_t *src = nullptr;
   auto fetch = [&](int slot) {
     if (fw.more()) {
-      if (fw.fresh) src = fw.row(in, fw.r * kRowsWarp + hl) + 2 * w.a;
-      const bool ok = w.on && fw.r * kRowsWarp + hl < H;
+      const int h = fw.r * kRowsWarp + hl;
+      if (fw.fresh) {
+        src = fw.row(in, h) + 2 * w.a;
+        copy8(&meta[warp][slot][0][lane], rope_position(p, fw.b, fw.l), p.pos64);
+        if (cached)
+          copy8(&meta[warp][slot][1][lane], p.slots + static_cast<long long>(fw.b) * p.L + fw.l, true);
+      }
+      const bool ok = w.on && h < H;
       copy16(&ring[warp][slot][0][lane], src, ok);
       copy16(&ring[warp][slot][1][lane], src + ab, ok);
       src += 2 * kRowsWarp * in.sh;
@@ -316,35 +351,23 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
 #pragma unroll
   for (int k = 0; k < S - 1; ++k) fetch(k);
   int slot = 0;
-  bool real = false, turn = false;
+  bool real = false, stored = false, turn = false;
   uint8_t *d0 = nullptr, *d1 = nullptr;   // where a row goes: the output, the cache
   float4 co[2], si[2];
   for (; cw.more(); cw.next(p)) {
+    copy_wait<S - 2>();
+    uint4 a = ring[warp][slot][0][lane], bb = ring[warp][slot][1][lane];
+    const int h = cw.r * kRowsWarp + hl;
     if (cw.fresh) {
-      const long long pos = rope_position(p, cw.b, cw.l);
-      const int h = cw.r * kRowsWarp + hl;
+      const long long pos = rope_position_of(p, &meta[warp][slot][0][lane]);
       real = pos >= 0 && pos < p.max_pos;   // else padding: left as it was
-      d0 = !is_v && out.ptr ? cw.row(out, h) + 2 * w.a : nullptr;
-      d1 = nullptr;
-      if (!is_q && p.kc) {
-        const long long slot_id = __ldg(p.slots + static_cast<long long>(cw.b) * p.L + cw.l);
-        if (slot_id >= 0 && slot_id < p.n_slots) {
-          long long page, in_page;
-          if (p.n_slots <= 0x7fffffffll) {   // (a 32-bit division is a third of the cost)
-            page = static_cast<unsigned>(slot_id) / static_cast<unsigned>(p.page_size);
-            in_page = static_cast<unsigned>(slot_id) % static_cast<unsigned>(p.page_size);
-          } else {
-            page = slot_id / p.page_size;
-            in_page = slot_id % p.page_size;
-          }
-          d1 = (is_v ? p.vc : p.kc) + 2 * (page * p.c_sp + in_page * p.c_st + h * p.c_sh + w.a);
-        }
-      }
+      if (want) d0 = cw.row(out, h) + 2 * w.a;
+      long long at = 0;
+      stored = cached && rope_slot(p, meta[warp][slot][1][lane], at);
+      d1 = (is_v ? p.vc : p.kc) + 2 * (at + h * p.c_sh + w.a);
       turn = w.turn && real && !is_v;
       if (turn) rope_angles(p, pos, w, co, si);
     }
-    copy_wait<S - 2>();
-    uint4 a = ring[warp][slot][0][lane], bb = ring[warp][slot][1][lane];
     slot = slot + 1 == S ? 0 : slot + 1;
     fetch(slot + S - 2 >= S ? slot - 2 : slot + S - 2);   // the slot read one row ago
     if (!real) continue;
@@ -358,13 +381,13 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
       if (turn) turn16<1, kInter>(x, co, si);
       pack16<DT>(x, a, bb);
     }
-    if (w.on && cw.r * kRowsWarp + hl < H) {
-      if (d0) {
+    if (w.on && h < H) {
+      if (want) {
         st16(d0, a);
         st16(d0 + ab, bb);
         d0 += 2 * kRowsWarp * out.sh;
       }
-      if (d1) {
+      if (stored) {
         st16(d1, a);
         st16(d1 + ab, bb);
         d1 += 2 * kRowsWarp * p.c_sh;
@@ -383,6 +406,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBwdBlocks)
     fa_rope_bwd_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kRowsWarp = 32 / kSeg, S = kRopeBwdStages, kWarps = kRopeThreads / 32;
   __shared__ uint4 ring[kWarps][S][4][32];
+  __shared__ long long meta[kWarps][S][32];   // position
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, hl = lane / kSeg;
   const bool is_q = static_cast<int>(blockIdx.x) < p.blocks_q;
   const unsigned me = (is_q ? blockIdx.x : blockIdx.x - p.blocks_q) * kWarps + warp;
@@ -400,7 +424,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBwdBlocks)
   if (w.on && weight) g = rope_weight<DT>(weight, w);
 
   RopeRun fw, cw;
-  fw.start(p, is_q, me, n, steps);
+  fw.start(p, me, n, steps);
   cw = fw;
   const uint8_t *sx = nullptr, *sy = nullptr;
   auto fetch = [&](int slot) {
@@ -409,6 +433,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBwdBlocks)
       if (fw.fresh) {
         sx = fw.row(in, h) + 2 * w.a;
         sy = fw.row(dy, h) + 2 * w.a;
+        copy8(&meta[warp][slot][lane], rope_position(p, fw.b, fw.l), p.pos64);
       }
       const bool ok = w.on && h < H;
       copy16(&ring[warp][slot][0][lane], sx, ok);
@@ -428,13 +453,13 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBwdBlocks)
   uint8_t *dst = nullptr;
   float4 co[2], si[2];
   for (; cw.more(); cw.next(p)) {
+    copy_wait<S - 2>();
     if (cw.fresh) {
-      const long long pos = rope_position(p, cw.b, cw.l);
+      const long long pos = rope_position_of(p, &meta[warp][slot][lane]);
       real = pos >= 0 && pos < p.max_pos;   // else padding, without an output
       dst = cw.row(dx, cw.r * kRowsWarp + hl) + 2 * w.a;
       if (w.turn && real) rope_angles(p, pos, w, co, si);
     }
-    copy_wait<S - 2>();
     Row16 x = unpack16<DT>(ring[warp][slot][0][lane], ring[warp][slot][1][lane]);
     Row16 y = unpack16<DT>(ring[warp][slot][2][lane], ring[warp][slot][3][lane]);
     slot = slot + 1 == S ? 0 : slot + 1;

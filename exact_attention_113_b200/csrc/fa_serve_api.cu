@@ -75,56 +75,70 @@ RopeParams rope_params(const fa_rope_args *a) {
 
 int rope_seg(int D) { return D > 64 ? 8 : (D > 32 ? 4 : (D > 16 ? 2 : 1)); }
 
-// Deals up to `blocks` blocks to the kinds of rows in proportion, at least one
-// each and no more than have a row for each lane, and cuts a token's steps in
-// chunks: whole tokens where a warp gets 16 of them, else fewer steps, so that
-// no warp has much more than its share.  0: too many rows (a 32-bit index
-// walks them).
-int rope_deal(RopeParams &r, int seg, int blocks, bool values) {
-  const int lanes = 32 / seg;   // rows of a step
+// Deals up to `blocks` blocks to three kinds of rows (query, key, value), of
+// which a token has the given numbers of steps: at least one to a kind that has
+// rows and no more than have a step for each warp.  A token's fixed work
+// (addresses, angles, slot) is about that of a step, so a kind's share goes by
+// its steps + 1 (the gradient at B2 L16384 H32/8 D128: 183 us, by its steps 200).
+void rope_deal(long long tokens, int blocks, const int (&steps)[3], int (&out)[3]) {
   constexpr int kWarps = kRopeThreads / 32;
-  const long long tokens = static_cast<long long>(r.B) * r.L;
-  const long long rows = static_cast<long long>(r.H) + r.H_kv + (values ? r.H_kv : 0);
-  auto steps = [&](int H) { return (H + lanes - 1) / lanes; };
-  if (tokens * steps(std::max(r.H, r.H_kv)) > 0x7fffffffll) return 0;
-  auto share = [&](int H, long long part) {
-    const long long most = (tokens * steps(H) + kWarps - 1) / kWarps;
-    return static_cast<int>(std::min(std::max(part, 1ll), most));
-  };
-  auto cut = [&](int H, int n, int &chunks, int &per) {
-    const long long fit = tokens * steps(H) / (16ll * kWarps * std::max(n, 1));
-    const int most = static_cast<int>(std::min<long long>(std::max(fit, 1ll), std::max(steps(H), 1)));
-    chunks = (std::max(steps(H), 1) + most - 1) / most;
-    per = (std::max(steps(H), 1) + chunks - 1) / chunks;
-    chunks = (std::max(steps(H), 1) + per - 1) / per;
-  };
-  r.blocks_k = share(r.H_kv, blocks * static_cast<long long>(r.H_kv) / rows);
-  const int rest = values ? r.blocks_k : 0;
-  r.blocks_q = share(r.H, blocks - r.blocks_k - rest);
-  cut(r.H, r.blocks_q, r.chunks_q, r.per_q);
-  cut(r.H_kv, r.blocks_k, r.chunks_k, r.per_k);
-  return r.blocks_q + r.blocks_k + rest;
+  long long all = 0;
+  for (int i = 0; i < 3; ++i) all += steps[i] ? steps[i] + 1 : 0;
+  for (int i = 2; i >= 0; --i) {
+    const long long most = (tokens * steps[i] + kWarps - 1) / kWarps;
+    const long long part = i == 0 ? blocks - out[1] - out[2] : blocks * (steps[i] + 1ll) / all;
+    out[i] = static_cast<int>(std::min(std::max(part, 1ll), most));
+  }
 }
+
+// Chunks of a token's steps: whole tokens where a warp gets 4 of them, else
+// fewer steps, so that no warp has much more than its share.
+void rope_cut(long long tokens, int steps, int blocks, int &chunks, int &per) {
+  steps = std::max(steps, 1);
+  const long long fit = tokens * steps / (4ll * (kRopeThreads / 32) * std::max(blocks, 1));
+  const int most = static_cast<int>(std::min<long long>(std::max(fit, 1ll), steps));
+  chunks = (steps + most - 1) / most;
+  per = (steps + chunks - 1) / chunks;
+  chunks = (steps + per - 1) / per;
+}
+
+constexpr long long kRopeMostSteps = 0x7fffffffll;   // 32-bit indexes walk them
 
 template <int kSeg, int DT>
 int launch_rope_fwd(RopeParams &r, cudaStream_t stream) {
-  const int blocks = rope_deal(r, kSeg, sms() * kRopeBlocks, r.vc != nullptr);
-  if (blocks == 0) return FA_ERR_SHAPE;
+  constexpr int kRows = 32 / kSeg;
+  const long long tokens = static_cast<long long>(r.B) * r.L;
+  const int kv = (r.H_kv + kRows - 1) / kRows;
+  const int steps[3] = {(r.H + kRows - 1) / kRows, kv, r.vc ? kv : 0};
+  if (tokens * std::max(steps[0], kv) > kRopeMostSteps) return FA_ERR_SHAPE;
+  int blocks[3];
+  rope_deal(tokens, sms() * kRopeBlocks, steps, blocks);
+  r.blocks_q = blocks[0];
+  r.blocks_k = blocks[1];
+  rope_cut(tokens, steps[0], blocks[0], r.chunks_q, r.per_q);
+  rope_cut(tokens, steps[1], blocks[1], r.chunks_k, r.per_k);
+  const unsigned grid = blocks[0] + blocks[1] + blocks[2];
   if (r.interleaved)
-    fa_rope_fwd_kernel<kSeg, DT, true><<<blocks, kRopeThreads, 0, stream>>>(r);
+    fa_rope_fwd_kernel<kSeg, DT, true><<<grid, kRopeThreads, 0, stream>>>(r);
   else
-    fa_rope_fwd_kernel<kSeg, DT, false><<<blocks, kRopeThreads, 0, stream>>>(r);
+    fa_rope_fwd_kernel<kSeg, DT, false><<<grid, kRopeThreads, 0, stream>>>(r);
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 template <int kSeg, int DT>
 int launch_rope_bwd(RopeParams &r, cudaStream_t stream) {
-  const int blocks = rope_deal(r, kSeg, sms() * kRopeBwdBlocks, false);
-  if (blocks == 0) return FA_ERR_SHAPE;
+  constexpr int kRows = 32 / kSeg;
+  const long long tokens = static_cast<long long>(r.B) * r.L;
+  const int steps[3] = {(r.H + kRows - 1) / kRows, (r.H_kv + kRows - 1) / kRows, 0};
+  if (tokens * std::max(steps[0], steps[1]) > kRopeMostSteps) return FA_ERR_SHAPE;
+  int blocks[3];
+  rope_deal(tokens, sms() * kRopeBwdBlocks, steps, blocks);
+  r.blocks_q = blocks[0];
+  r.blocks_k = blocks[1];
   if (r.interleaved)
-    fa_rope_bwd_kernel<kSeg, DT, true><<<blocks, kRopeThreads, 0, stream>>>(r);
+    fa_rope_bwd_kernel<kSeg, DT, true><<<blocks[0] + blocks[1], kRopeThreads, 0, stream>>>(r);
   else
-    fa_rope_bwd_kernel<kSeg, DT, false><<<blocks, kRopeThreads, 0, stream>>>(r);
+    fa_rope_bwd_kernel<kSeg, DT, false><<<blocks[0] + blocks[1], kRopeThreads, 0, stream>>>(r);
   if (r.dwq || r.dwk) fa_rope_dw_kernel<<<dim3(2, (r.D + 31) / 32), 1024, 0, stream>>>(r);
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
