@@ -655,7 +655,8 @@ def flash_fwd_host(q, k, v, scale=None, causal=False, window_left=-1, window_rig
 
 # ------------------------------------------------------------ serving
 # These run for every layer of a decoding step, where a call's host time
-# counts: their checks and allocations are compiled (csrc/fa_torch.cpp).
+# counts: their checks and allocations are compiled (csrc/fa_torch.cpp).  With
+# a ``stream`` the call runs and allocates there, else on the current stream.
 EXT_PATH = os.path.join(PKG, "lib", "_fa_torch.so")
 _ext = None
 
@@ -702,8 +703,9 @@ def paged_plan(q_lens, ctx_lens, block_table, free_pages, page_size, num_tokens,
     in place from free_pages (int32, taken from index 0); num_tokens: the
     capacity of positions and slots (at least the new tokens; the rest, a
     captured graph's padding, gets -1).  ``out``: a PagedPlan to write into;
-    otherwise its tensors share one allocation.  Nothing is read back:
-    counts[2] > 0 tells that pages ran out."""
+    otherwise its tensors share one allocation.  They may not overlap the
+    inputs: ctx_lens cannot be out.kv_lens.  Nothing is read back: counts[2] > 0
+    tells that pages ran out."""
     r = (_ext or _serving()).paged_plan(q_lens, ctx_lens, block_table, free_pages, page_size,
                                         num_tokens, out, _handle(stream))
     return PagedPlan._make(r) if out is None else out

@@ -102,6 +102,16 @@ void rope_cut(long long tokens, int steps, int blocks, int &chunks, int &per) {
   chunks = (steps + per - 1) / per;
 }
 
+// Bytes of an array, and whether two arrays share some.
+struct Span {
+  uintptr_t at, end;
+};
+Span span(const void *p, long long n, int size) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+  return {a, a + static_cast<uintptr_t>(n) * size};
+}
+bool meet(const Span &a, const Span &b) { return a.at < b.end && b.at < a.end; }
+
 constexpr long long kRopeMostSteps = 0x7fffffffll;   // 32-bit indexes walk them
 
 template <int kSeg, int DT>
@@ -152,7 +162,7 @@ extern "C" int fa_paged_plan(const int *q_lens, const int *ctx_lens, int *block_
                              long long table_stride, const int *free_pages, int n_free, int B,
                              int max_pages, int page_size, int num_tokens, int *cu_q, int *kv_lens,
                              int *positions, long long *slots, int *counts, cudaStream_t stream) {
-  if (B < 1 || n_free < 0 || max_pages < 0 || num_tokens < 0) return FA_ERR_SHAPE;
+  if (B < 1 || B > kMaxLen || n_free < 0 || max_pages < 0 || num_tokens < 0) return FA_ERR_SHAPE;
   if (page_size < 1 || page_size > kMaxLen || table_stride < max_pages) return FA_ERR_ARG;
   if (!q_lens || !ctx_lens || !cu_q || !kv_lens || !counts || (max_pages > 0 && !block_table) ||
       (n_free > 0 && !free_pages) || (num_tokens > 0 && (!positions || !slots)))
@@ -160,6 +170,21 @@ extern "C" int fa_paged_plan(const int *q_lens, const int *ctx_lens, int *block_
   if (!al(q_lens, 4) || !al(ctx_lens, 4) || !al(block_table, 4) || !al(free_pages, 4) ||
       !al(cu_q, 4) || !al(kv_lens, 4) || !al(positions, 4) || !al(slots, 8) || !al(counts, 4))
     return FA_ERR_ALIGN;
+  {
+    // every block reads all lengths while others write: what is written has
+    // to lie apart (kv_lens on the next step's ctx_lens, for one, would not do)
+    const long long rows = (B - 1) * table_stride + max_pages;
+    const Span in[3] = {span(q_lens, B, 4), span(ctx_lens, B, 4), span(free_pages, n_free, 4)};
+    const Span out[6] = {span(block_table, max_pages ? rows : 0, 4), span(cu_q, B + 1ll, 4),
+                         span(kv_lens, B, 4), span(positions, num_tokens, 4),
+                         span(slots, num_tokens, 8), span(counts, 3, 4)};
+    for (int i = 0; i < 6; ++i) {
+      for (const Span &x : in)
+        if (meet(out[i], x)) return FA_ERR_ARG;
+      for (int j = 0; j < i; ++j)
+        if (meet(out[i], out[j])) return FA_ERR_ARG;
+    }
+  }
   PlanParams p;
   p.q_lens = q_lens;
   p.ctx_lens = ctx_lens;

@@ -73,10 +73,22 @@ struct Device {
   }
 };
 
-cudaStream_t stream_of(PyObject *handle, c10::DeviceIndex dev) {
-  if (handle == Py_None) return c10::cuda::getCurrentCUDAStream(dev).stream();
-  return reinterpret_cast<cudaStream_t>(integer(handle));
-}
+// The call's stream: the given one, which also becomes the current one for the
+// call, so that what is allocated here belongs to it (a workspace freed on
+// return is then not handed to another stream's kernels while this call's
+// still run), or the current one.
+struct Stream {
+  c10::cuda::OptionalCUDAStreamGuard guard;
+  cudaStream_t s;
+  Stream(PyObject *handle, c10::DeviceIndex dev) {
+    if (handle == Py_None) {
+      s = c10::cuda::getCurrentCUDAStream(dev).stream();
+    } else {
+      s = reinterpret_cast<cudaStream_t>(integer(handle));
+      guard.reset_stream(c10::cuda::getStreamFromExternal(s, dev));
+    }
+  }
+};
 
 template <typename F>
 void call(const char *where, F &&f) {
@@ -190,6 +202,7 @@ PyObject *paged_plan(PyObject *, PyObject *const *a, Py_ssize_t na) {
   at::Tensor o[5];   // cu_q, kv_lens, positions, slots, counts
   const int64_t n[5] = {B + 1, B, T, T, 3};
   c10::cuda::CUDAGuard guard(dev.index);
+  const Stream stream(a[7], dev.index);
   if (a[6] == Py_None) {
     // one allocation, the 8-byte values first
     const at::Tensor buf = empty({2ll * T + T + 2ll * B + 4}, q, at::kInt);
@@ -209,7 +222,6 @@ PyObject *paged_plan(PyObject *, PyObject *const *a, Py_ssize_t na) {
       o[i] = *t;
     }
   }
-  const cudaStream_t s = stream_of(a[7], dev.index);
   call("fa_paged_plan", [&] {
     return fa_paged_plan(static_cast<int *>(q->data_ptr()), static_cast<int *>(ctx->data_ptr()),
                          static_cast<int *>(table->data_ptr()), tb.stride,
@@ -217,7 +229,7 @@ PyObject *paged_plan(PyObject *, PyObject *const *a, Py_ssize_t na) {
                          page_size, T, static_cast<int *>(o[0].data_ptr()),
                          static_cast<int *>(o[1].data_ptr()), static_cast<int *>(o[2].data_ptr()),
                          static_cast<long long *>(o[3].data_ptr()),
-                         static_cast<int *>(o[4].data_ptr()), s);
+                         static_cast<int *>(o[4].data_ptr()), stream.s);
   });
   PyObject *r = PyTuple_New(5);
   for (int i = 0; r && i < 5; ++i) PyTuple_SET_ITEM(r, i, THPVariable_Wrap(std::move(o[i])));
@@ -302,6 +314,7 @@ PyObject *qk_norm_rope(PyObject *, PyObject *const *a, Py_ssize_t na) {
                                   "k_out", "v", "k_cache", "v_cache", "slots"};
   for (int i = 0; i < 12; ++i) dev.on(all[i], names[i]);
   c10::cuda::CUDAGuard guard(dev.index);
+  const Stream stream(a[14], dev.index);
   at::Tensor q_out, k_out;
   if (!qo) {
     q_out = empty(q->sizes(), q, type);
@@ -313,8 +326,7 @@ PyObject *qk_norm_rope(PyObject *, PyObject *const *a, Py_ssize_t na) {
   }
   r.q_out = rows_of(qo, "q_out", q->sizes(), type);
   if (ko) r.k_out = rows_of(ko, "k_out", k->sizes(), type);
-  const cudaStream_t s = stream_of(a[14], dev.index);
-  call("fa_qk_norm_rope", [&] { return fa_qk_norm_rope(&r, s); });
+  call("fa_qk_norm_rope", [&] { return fa_qk_norm_rope(&r, stream.s); });
   PyObject *res = PyTuple_New(2);
   if (!res) return nullptr;
   if (q_out.defined()) {
@@ -353,6 +365,7 @@ PyObject *qk_norm_rope_bwd(PyObject *, PyObject *const *a, Py_ssize_t na) {
                                   "dk_out", "dq", "dk", "workspace"};
   for (int i = 0; i < 11; ++i) dev.on(all[i], names[i]);
   c10::cuda::CUDAGuard guard(dev.index);
+  const Stream stream(a[13], dev.index);
   at::Tensor o[4];   // dq, dk, dq_weight, dk_weight
   if (dq) o[0] = *dq; else o[0] = empty(q->sizes(), q, type);
   if (dk) o[1] = *dk; else o[1] = empty(k->sizes(), q, type);
@@ -368,12 +381,12 @@ PyObject *qk_norm_rope_bwd(PyObject *, PyObject *const *a, Py_ssize_t na) {
     own = empty({static_cast<int64_t>(fa_qk_norm_rope_bwd_workspace_bytes(r.D))}, q, at::kByte);
     ws = &own;
   }
-  const cudaStream_t s = stream_of(a[13], dev.index);
   call("fa_qk_norm_rope_bwd", [&] {
     return fa_qk_norm_rope_bwd(&r, rq, rk, wq ? static_cast<float *>(o[2].data_ptr()) : nullptr,
                                wk ? static_cast<float *>(o[3].data_ptr()) : nullptr,
                                ws ? ws->data_ptr() : nullptr,
-                               ws ? static_cast<size_t>(ws->numel()) * ws->element_size() : 0, s);
+                               ws ? static_cast<size_t>(ws->numel()) * ws->element_size() : 0,
+                               stream.s);
   });
   PyObject *res = PyTuple_New(4);
   for (int i = 0; res && i < 4; ++i) {
@@ -419,6 +432,7 @@ PyObject *flash_fwd_paged(PyObject *, PyObject *const *a, Py_ssize_t na) {
                                  "lse", "workspace"};
   for (int i = 0; i < 9; ++i) dev.on(all[i], names[i]);
   c10::cuda::CUDAGuard guard(dev.index);
+  const Stream stream(a[14], dev.index);
   at::Tensor o, l, own;
   if (!out) {
     o = empty(q->sizes(), q, type);
@@ -439,7 +453,6 @@ PyObject *flash_fwd_paged(PyObject *, PyObject *const *a, Py_ssize_t na) {
     own = empty({static_cast<int64_t>(fa_paged_workspace_bytes(D)) + 1}, q, at::kByte);
     ws = &own;
   }
-  const cudaStream_t s = stream_of(a[14], dev.index);
   call("fa_fwd_paged", [&] {
     return fa_fwd_paged(q->data_ptr(), q->stride(0), q->stride(1), k->data_ptr(), v->data_ptr(), c.sp,
                         c.st, c.sh, static_cast<int *>(table->data_ptr()), tb.stride,
@@ -447,7 +460,8 @@ PyObject *flash_fwd_paged(PyObject *, PyObject *const *a, Py_ssize_t na) {
                         out->data_ptr(), out->stride(0), out->stride(1),
                         lse ? static_cast<float *>(lse->data_ptr()) : nullptr, T, B, H, H_kv, D,
                         c.pages, c.page_size, tb.columns, scale, causal, wl, wr, dtype,
-                        ws->data_ptr(), static_cast<size_t>(ws->numel()) * ws->element_size(), s);
+                        ws->data_ptr(), static_cast<size_t>(ws->numel()) * ws->element_size(),
+                        stream.s);
   });
   PyObject *res = PyTuple_New(2);
   if (!res) return nullptr;

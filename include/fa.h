@@ -390,8 +390,9 @@ int fa_fwd_splitkv_static(const void *q, const void *k, const void *v, void *out
  *                table entries get -1, or the table's columns)
  * num_tokens is the capacity of positions and slots: a padded batch of a
  * captured graph has more than the requests' tokens, and tokens beyond it
- * are not written.  FA_ERR_ARG for page_size < 1 or table_stride <
- * max_pages; pointers to arrays with no elements may be NULL.
+ * are not written.  What is written may not overlap anything else (the next
+ * step's ctx_lens is a copy of kv_lens, or the other of two).  FA_ERR_ARG for
+ * such an overlap, page_size < 1 or table_stride < max_pages; pointers to arrays with no elements may be NULL.
  */
 int fa_paged_plan(const int *q_lens, const int *ctx_lens, int *block_table,
                   long long table_stride, const int *free_pages, int n_free, int B, int max_pages,

@@ -350,3 +350,26 @@ def test_serving_steps(dtype, page, wl):
         train, _ = fa.flash_fwd(qo, ko, vt, causal=True, window_left=wl)
         assert ((train[0].transpose(0, 1).double() - got).abs()
                 <= 2 * ref.attention_bound(want, mag, tot, dtype)).all()
+
+
+def test_given_stream_owns_what_is_allocated():
+    # memory of another stream's pool could be in use there when this call runs
+    def stream_of(t):
+        for seg in torch.cuda.memory_snapshot():
+            if seg["address"] <= t.data_ptr() < seg["address"] + seg["total_size"]:
+                return seg["stream"]
+
+    b = Batch([1] * 3, [300] * 3, 8, 2, 128, BF16, 16, seed=40)
+    cs, pos = torch.rand(400, 128, device="cuda"), (b.kv_lens - 1).repeat(b.T)[: b.T]
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    out, lse = fa.flash_fwd_paged(b.q, b.k, b.v, b.table, b.cu_q, b.kv_lens, stream=st)
+    q2, k2 = fa.qk_norm_rope(b.q, b.q[:, :2], None, None, cs, pos, stream=st)
+    w = torch.ones(128, dtype=BF16, device="cuda")
+    grads = fa.qk_norm_rope_bwd(b.q, b.q[:, :2], w, w, cs, pos, b.q, b.q[:, :2], stream=st)
+    plan = fa.paged_plan(b.kv_lens, b.kv_lens.clone(), b.table.clone(), b.kv_lens.clone(), 16, 9,
+                         stream=st)
+    for t in (out, lse, q2, k2, *grads, *plan):
+        assert stream_of(t) == st.cuda_stream
+    assert torch.cuda.current_stream() == torch.cuda.default_stream()
+    st.synchronize()

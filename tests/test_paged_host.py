@@ -192,3 +192,16 @@ def test_wrappers_refuse_bad_tensors(lib):
         fa.paged_plan(kv.long(), kv, table, kv, 16, 8)
     with pytest.raises(ValueError):
         fa.paged_plan(kv, kv, table[:1], kv, 16, 8)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(kv="ctx"), dict(kv="q"), dict(cu="ctx"), dict(pos="slots"), dict(counts="cu"),
+    dict(table="free"), dict(slots="table"),
+])
+def test_plan_refuses_overlap(lib, kw):
+    # every array on a page of its own but one, which shares its last bytes
+    names = ("q", "ctx", "table", "free", "cu", "kv", "pos", "slots", "counts")
+    at = {n: 4096 * (i + 1) for i, n in enumerate(names)}
+    for a, b in kw.items():
+        at[a] = at[b]
+    assert _plan(**at) == -6

@@ -106,3 +106,20 @@ def test_graph_replay_with_other_lengths():
     torch.cuda.synchronize()
     got = (out.cu_q, out.kv_lens, out.positions, out.slots, table, out.counts)
     assert [t.tolist() for t in got] == list(want)
+
+
+def test_alternating_outputs_and_refused_overlap():
+    # each step's contexts are the lengths that the step before it wrote
+    q, table = _t([1, 30, 2]), torch.full((3, 8), -1, dtype=torch.int32, device="cuda")
+    free, c = _t(list(range(24))), _t([0, 0, 0])
+    outs = [fa.paged_plan(_t([0] * 3), c, table, free, 16, 33) for _ in range(2)]
+    rows, ctx, taken = table.tolist(), [0, 0, 0], 0
+    for step in range(4):
+        p = fa.paged_plan(q, c, table, free[taken:].clone(), 16, 33, out=outs[step % 2])
+        want = ref.plan([1, 30, 2], ctx, rows, list(range(24))[taken:], 16, 33)
+        assert p.slots.tolist() == want[3] and table.tolist() == want[4]
+        assert p.kv_lens.tolist() == want[1] and p.counts.tolist() == want[5]
+        c, ctx, rows = p.kv_lens, want[1], want[4]
+        taken += want[5][1]
+    with pytest.raises(fa.FaError):
+        fa.paged_plan(q, outs[0].kv_lens, table, free, 16, 33, out=outs[0])
