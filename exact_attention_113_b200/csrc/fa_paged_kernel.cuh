@@ -47,6 +47,11 @@ constexpr int kSchedWarp = 11;       // walks the work, loads Q
 constexpr int kPagedMinUnits = 2;    // cost a CTA gets at least
 constexpr int kPagedRows = 2 * kBM;  // rows of a work item
 constexpr int kItemRing = 3;         // items announced ahead
+// A single tile of at most this many rows (decoding) takes TMEM in the layout of a
+// matrix fragment: four lanes share a row, 32 of a block's 128 exponentials each.
+// One warp's 128 of a lane had set the pace (128 requests over 500 tokens, H32/8
+// D128: 76 us so, 57 shared; 8 over 1000: 24.5 and 22).
+constexpr int kFewRows = 8;
 
 struct PagedParams {
   CUtensorMap tm_q;   // (D, H, total_q), box (cols, G, TQ)
@@ -460,6 +465,39 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
       : "r"(bar), "r"(parity)
       : "memory");
   return ok != 0;
+}
+
+// 16 lanes of TMEM in the layout of a matrix fragment.  Load, 64 columns: r[4j],
+// r[4j + 1] are columns 8j + 2c, 8j + 2c + 1 of TMEM lane g, r[4j + 2], r[4j + 3]
+// of lane g + 8, with g = lane / 4, c = lane % 4.  Store, 64 columns: r[2j] is
+// column 4j + c of lane g, r[2j + 1] of lane g + 8.
+__device__ __forceinline__ void tmem_ld_rows16(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, "
+      "[%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+        "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+        "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+        "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+        "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_rows16(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
+      ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+      "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]),
+      "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
+      "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
 }
 
 __device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
@@ -1040,6 +1078,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int u = warp >> 2;                 // warpgroup
     const int r = tid & 127;                 // tile row = TMEM lane
     const int r_tok = r / p.group, r_head = r - (r / p.group) * p.group;
+    const int few_tok = (lane >> 2) / p.group;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_base + u * 128u;
     const uint32_t tP = kSplitP ? tmem + lane_base + 384u + u * 64u : tS;
@@ -1065,7 +1104,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int first = t.first + tile * p.tile_q, last = first + nt - 1;
       const bool valid = r_tok < nt;         // (r_tok >= tile_q: rows behind the tile)
       const bool busy = __any_sync(0xffffffffu, valid);
-      const int x = first + r_tok;
+      const bool few = single && nt * p.group <= kFewRows;
+      const int x = first + (few ? few_tok : r_tok);   // this lane's row of the softmax
       const int row_lo = p.wl < 0 ? 0 : x - p.wl;
       const int row_hi = p.wr < 0 ? t.kv_len - 1 : min(t.kv_len - 1, x + p.wr);
       const int full_lo = p.wl < 0 ? 0 : last - p.wl;
@@ -1077,6 +1117,88 @@ __global__ void __launch_bounds__(kThreads, 1)
 
       float m_use = -INFINITY;   // reference max, log2 units of the scaled scores
       float l = 0.0f;            // normaliser relative to m_use
+      if (few && busy) {
+        const bool real = few_tok < nt;
+        for (int n = 0; n < n_blocks; ++n, ++ns) {
+          const int k0 = (j0 + n * jstep) * kBN;
+          ok = mbar_wait_warp(smem_u32(&bars->s_full[u]), ns & 1, abort_flag);
+          if (!ok) break;
+          tc_fence_after_sync();
+          float2 s[16];
+          {
+            uint32_t sr[2][32];
+            tmem_ld_rows16(tS, sr[0]);
+            tmem_ld_rows16(tS + 64, sr[1]);
+            tmem_wait_ld();
+            reg_dep(sr[0]);
+            reg_dep(sr[1]);
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              s[j] = make_float2(__uint_as_float(sr[j >> 3][(j & 7) * 4]),
+                                 __uint_as_float(sr[j >> 3][(j & 7) * 4 + 1]));
+          }
+          if (kSplitP) {   // S may be overwritten from here on
+            tc_fence_before_sync();
+            arrive(&bars->s_free[u]);
+          }
+          if (k0 < full_lo || k0 + kBN - 1 > full_hi) {
+            const int at = k0 + 2 * (lane & 3), lo_c = row_lo - at, hi_c = row_hi - at;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              if (8 * j < lo_c || 8 * j > hi_c) s[j].x = -INFINITY;
+              if (8 * j + 1 < lo_c || 8 * j + 1 > hi_c) s[j].y = -INFINITY;
+            }
+          }
+          float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+          for (int j = 0; j < 16; ++j) mx[j & 1] = fmax3(mx[j & 1], s[j].x, s[j].y);
+          float m = fmaxf(mx[0], mx[1]);
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+          m = m == -INFINITY ? -INFINITY : m * sl2;
+          float alpha = 1.0f;
+          const bool rescale = __any_sync(0xffffffffu, m > m_use + kRescaleThreshold);
+          if (rescale) {
+            const float m_upd = fmaxf(m_use, m);
+            alpha = (m_upd == -INFINITY) ? 1.0f : ex2(m_use - m_upd);
+            m_use = m_upd;
+            l *= alpha;
+          }
+          const float nm = !real ? -INFINITY : (m_use == -INFINITY ? 0.0f : -m_use);
+          float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          uint32_t pk[32];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float2 e = __ffma2_rn(s[j], sl2v, make_float2(nm, nm));
+            const float2 pp = make_float2(ex2(e.x), ex2(e.y));
+            ls[j & 1] = __fadd2_rn(ls[j & 1], pp);
+            pk[2 * j] = pack2<DT>(pp.x, pp.y);
+            pk[2 * j + 1] = 0u;
+          }
+          if (kSplitP && ns > 0) {
+            ok = mbar_wait_warp(smem_u32(&bars->pv_done[u]), (ns - 1) & 1, abort_flag);
+            if (!ok) break;
+            tc_fence_after_sync();
+          }
+          tmem_st_rows16(tP, pk);
+          if (kSplitP && n == 0) {   // zeros behind, for the power
+#pragma unroll
+            for (int j = 0; j < 16; ++j) pk[2 * j] = 0u;
+            tmem_st_rows16(tP + (16u << 16), pk);
+          }
+          if (rescale && n > 0)
+            scale_o_row<D>(tO, __shfl_sync(0xffffffffu, alpha, (4 * lane) & 31));
+          l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
+          tmem_wait_st();
+          tc_fence_before_sync();
+          arrive(&bars->p_full[u]);
+        }
+        // a lane holds the row of its TMEM lane again (the first 8)
+        l += __shfl_xor_sync(0xffffffffu, l, 1);
+        l += __shfl_xor_sync(0xffffffffu, l, 2);
+        l = __shfl_sync(0xffffffffu, l, (4 * lane) & 31);
+        m_use = __shfl_sync(0xffffffffu, m_use, (4 * lane) & 31);
+      } else {
       for (int n = 0; n < n_blocks; ++n, ++ns) {
         const int k0 = (j0 + n * jstep) * kBN;
         ok = mbar_wait_warp(smem_u32(&bars->s_full[u]), ns & 1, abort_flag);
@@ -1235,6 +1357,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_before_sync();
         arrive(&bars->p_full[u]);
+      }
       }
       if (ok && n_blocks > 0) {
         ok = mbar_wait_warp(smem_u32(&bars->pv_done[u]), (ns - 1) & 1, abort_flag);
