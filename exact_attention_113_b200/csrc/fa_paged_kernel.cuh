@@ -509,7 +509,8 @@ __device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
 // workspace, whatever it held) the count is 0, and the last arrival leaves 0.
 __device__ __forceinline__ bool paged_ticket(const PagedParams &p, PagedCut cut) {
   unsigned long long *at = p.ticket + cut.cta0;
-  unsigned long long old = *reinterpret_cast<volatile unsigned long long *>(at);
+  // tried first: that this is the last part, which the joining waits for
+  unsigned long long old = (p.call << 16) | static_cast<unsigned>(cut.parts - 1);
   while (true) {
     const unsigned long long n = ((old >> 16) == p.call ? (old & 0xffffull) : 0ull) + 1;
     const bool last = n == static_cast<unsigned long long>(cut.parts);
@@ -567,15 +568,12 @@ __device__ __forceinline__ void paged_merge(const PagedParams &p, const PagedIte
     const int rr = (rb - tile * n0) * 32 + lane % R;   // row within the tile
     const bool valid = rr < (tile ? rows1 : rows0);    // (other rows were not written)
     const size_t row = static_cast<size_t>(tile * kBM + rr);
-    float m = -INFINITY;
-    if (valid)
-      for (int i = mine; i < cut.parts; i += share)
-        m = fmaxf(m, __ldcg(&p.ws_ml[static_cast<size_t>(slot_of(i)) * kPagedRows + row]).x);
-    for (int d = R; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    const float m_sub = m == -INFINITY ? 0.0f : m;
-    float acc[16], l = 0.0f;
+    // one pass, (m, l, O) raised as it goes, so that all loads are under way at once
+    float m = -INFINITY, acc[16], l = 0.0f;
 #pragma unroll
     for (int v = 0; v < 16; ++v) acc[v] = 0.0f;
+    // both sides of a join relative to m_new (no visible key: weight 0)
+    auto weight = [](float m_old, float m_new) { return ex2(m_old - (m_new == -INFINITY ? 0.0f : m_new)); };
     if (valid) {
 #pragma unroll 2
       for (int i = mine; i < cut.parts; i += share) {
@@ -584,22 +582,32 @@ __device__ __forceinline__ void paged_merge(const PagedParams &p, const PagedIte
         float4 x[4];
 #pragma unroll
         for (int v = 0; v < 4; ++v) x[v] = __ldcg(o + v * kPagedRows);
-        const float w = ex2(ml.x - m_sub);   // a part without a visible key: 0
-        l += w * ml.y;
+        const float m_new = fmaxf(m, ml.x), a = weight(m, m_new), w = weight(ml.x, m_new);
+        m = m_new;
+        l = l * a + w * ml.y;
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
-          acc[4 * v] += w * x[v].x;
-          acc[4 * v + 1] += w * x[v].y;
-          acc[4 * v + 2] += w * x[v].z;
-          acc[4 * v + 3] += w * x[v].w;
+          acc[4 * v] = acc[4 * v] * a + w * x[v].x;
+          acc[4 * v + 1] = acc[4 * v + 1] * a + w * x[v].y;
+          acc[4 * v + 2] = acc[4 * v + 2] * a + w * x[v].z;
+          acc[4 * v + 3] = acc[4 * v + 3] * a + w * x[v].w;
         }
       }
     }
     __syncwarp();
-    for (int d = R; d < 32; d <<= 1) {
-      l += __shfl_xor_sync(0xffffffffu, l, d);
+    if (R < 32) {
+      float top = m;
+      for (int d = R; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      const float w = weight(m, top);
+      m = top;
+      l *= w;
 #pragma unroll
-      for (int v = 0; v < 16; ++v) acc[v] += __shfl_xor_sync(0xffffffffu, acc[v], d);
+      for (int v = 0; v < 16; ++v) acc[v] *= w;
+      for (int d = R; d < 32; d <<= 1) {
+        l += __shfl_xor_sync(0xffffffffu, l, d);
+#pragma unroll
+        for (int v = 0; v < 16; ++v) acc[v] += __shfl_xor_sync(0xffffffffu, acc[v], d);
+      }
     }
     if (valid && mine == 0) {
       const float inv = l > 0.0f ? 1.0f / l : 0.0f;
@@ -718,8 +726,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   regs_dec<RegSplit::kSmall>();
   if (warp == kSchedWarp) {
     // =================================================== schedule and Q
-    // Items are announced up to kItemRing ahead of their last reader, one
-    // ahead of their Q: a tile with key blocks takes the next of two Q slots.
+    // Items are announced up to kItemRing ahead of their last reader, from the
+    // second on one ahead of their Q: a tile with key blocks takes the next of two Q slots.
     walk.end = bars->setup.end;
     PagedItem t, ahead;
     int nq = 0, k = 0;
@@ -733,10 +741,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) {
         bars->item[s] = it;
         mbar_arrive(smem_u32(&bars->item_full[s]));
-        if (more && it.slot >= 0) {   // (read when the part is finished)
-          bars->cut[it.slot] = walk.cut_of(cuts);
-          mbar_arrive(smem_u32(&bars->cut_full[it.slot]));
-        }
       }
       __syncwarp();
       ++k;
@@ -773,11 +777,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       ++nq;
     };
-    bool more = announce(t);
-    while (ok && more) {
-      more = announce(ahead);
-      if (ok && t.hi0 > t.lo0) load(t.h, t.tok0, t.nt0);
-      if (ok && t.hi1 > t.lo1) load(t.h, t.tok0 + p.tile_q, t.nt1);
+    // the first item's Q goes before the second item is looked for (with the
+    // order of the others its product began 1.5 us later)
+    for (int i = 0; ok; ++i) {
+      const bool more = announce(ahead);
+      if (i == 0) t = ahead;
+      if (ok && i != 1 && t.h >= 0) {
+        if (t.hi0 > t.lo0) load(t.h, t.tok0, t.nt0);
+        if (ok && t.hi1 > t.lo1) load(t.h, t.tok0 + p.tile_q, t.nt1);
+      }
+      if (!ok || !more) break;
+      if (ahead.slot >= 0 && lane == 0) {   // (read when the part is finished)
+        bars->cut[ahead.slot] = walk.cut_of(cuts);
+        mbar_arrive(smem_u32(&bars->cut_full[ahead.slot]));
+      }
+      __syncwarp();
       t = ahead;
     }
     if (!ok)   // let the copies in flight land before the CTA exits
@@ -1459,7 +1473,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (t.slot >= 0) {
         // a part: whoever finishes the item's last one joins them all
-        __threadfence();
+        // (one thread's fences order the CTA's rows, which it has seen arrive)
         arrive(&bars->part_done);
         if (tid == 0) {
           ok = mbar_wait(smem_u32(&bars->part_done), n_part & 1, abort_flag) &&
@@ -1478,7 +1492,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         ++n_part;
         if (bars->is_last) {
-          __threadfence();
           paged_merge<D, DT>(p, t, bars->cut[t.slot], warp, 8);
         }
         // (is_last is written again only after all eight warps have arrived
