@@ -12,7 +12,7 @@
 // 128-row tile holds TQ = floor(128 / G) tokens of all G heads (row r is
 // token r / G, head r % G): a key block is read once for the whole group.
 // Work: a (request, K/V head, pair of tiles) reads `blocks` key blocks of
-// 128 and costs blocks + 1.  The costs of all of them form one line, cut in
+// 128 and costs that many and the item's own.  The costs form one line, cut in
 // equal pieces, one per CTA (one CTA per SM), so that one long request, many
 // short ones and causal triangles all fill the device.  A CTA walks its
 // piece, whole items and, at the ends, parts of two items; parts leave an
@@ -44,7 +44,7 @@
 namespace fa {
 
 constexpr int kSchedWarp = 11;       // walks the work, loads Q
-constexpr int kPagedMinUnits = 2;    // cost a CTA gets at least
+constexpr int kPagedMinUnits = 3;    // cost a CTA gets at least (4: single tokens 2 us slower)
 constexpr int kPagedRows = 2 * kBM;  // rows of a work item
 constexpr int kItemRing = 3;         // items announced ahead
 // A single tile of at most this many rows (decoding) takes TMEM in the layout of a
@@ -118,22 +118,27 @@ __device__ __forceinline__ int paged_blocks(const PagedParams &p, const PagedReq
   return khi < klo ? 0 : khi / kBN - klo / kBN + 1;
 }
 
-// Cost of an item on the work line: a block of a pair takes about twice as
-// long as one of a single tile (2.2 against 1.2 us at D 128), and an item about
-// a block more.  before(off): the item's blocks that lie before a cut at off.
+// Cost of an item on the work line.  Measured: a block of a pair takes 1.8 us at
+// D 64 and 2.4 at D 128, one of a single tile 0.7 to 0.85 and 1.4; an item's
+// beginning and end (first softmax, last PV, epilogue) 2 to 4 us, of few rows 1
+// to 2.4.  (Against one block for an item: 8 chunks of up to 512 67 -> 62 us, 4
+// decoding over 4k 24 -> 21.)  before(off): the item's blocks that lie before a
+// cut at off.
 struct PagedCost {
-  int blocks, per, cost;   // cost = per * (blocks + 1)
+  int blocks, per, cost;   // cost = per * blocks + item()
+  __device__ __forceinline__ int item() const { return cost - per * blocks; }
   __device__ __forceinline__ int before(int off) const {
-    return off >= cost ? blocks : max((per == 2 ? off >> 1 : off) - 1, 0);
+    return off >= cost ? blocks : max(off - item(), 0) >> (per - 1);
   }
   // the largest off before which no block lies
-  __device__ __forceinline__ int snap() const { return 2 * per - 1; }
+  __device__ __forceinline__ int snap() const { return item() + per - 1; }
 };
 __device__ __forceinline__ PagedCost paged_cost(const PagedParams &p, const PagedReq &r, int pair) {
   PagedCost c;
   c.blocks = paged_blocks(p, r, pair);
-  c.per = r.q_len - pair * 2 * p.tile_q > p.tile_q ? 2 : 1;
-  c.cost = c.per * (c.blocks + 1);
+  const int n = r.q_len - pair * 2 * p.tile_q;
+  c.per = n > p.tile_q ? 2 : 1;
+  c.cost = c.per * c.blocks + (n * p.group <= kFewRows ? 2 : 4);
   return c;
 }
 
@@ -1237,8 +1242,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         } else {
-          const bool full = k0 >= full_lo && k0 + kBN - 1 <= full_hi;
-          auto load_s = [&](float (&sv)[kBN]) {
+          auto load_s = [&](float (&sv)[kBN], auto masked) {
             uint32_t sr[4][32];
             tmem_ld_x32(tS + 0, sr[0]);
             tmem_ld_x32(tS + 32, sr[1]);
@@ -1251,11 +1255,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             reg_dep(sr[3]);
 #pragma unroll
             for (int c = 0; c < kBN; ++c) sv[c] = __uint_as_float(sr[c >> 5][c & 31]);
-            if (!full) {
-              const int lo_c = row_lo - k0, hi_c = row_hi - k0;
+            if constexpr (!decltype(masked)::value) return;
+            if (k0 + kBN - 1 > full_hi) {   // some row's last key is in the block
+              const int hi_c = row_hi - k0;
 #pragma unroll
               for (int c = 0; c < kBN; ++c)
-                if (c < lo_c || c > hi_c) sv[c] = -INFINITY;
+                if (c > hi_c) sv[c] = -INFINITY;
+            }
+            if (k0 < full_lo) {             // some row's window begins in it
+              const int lo_c = row_lo - k0;
+#pragma unroll
+              for (int c = 0; c < kBN; ++c)
+                if (c < lo_c) sv[c] = -INFINITY;
             }
           };
           float alpha = 1.0f;
@@ -1302,7 +1313,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ls[0] = ls[1] = make_float2(0.f, 0.f);
           if constexpr (kSplitP) {
             float s[kBN];
-            load_s(s);
+            load_s(s, std::true_type{});
             // S may be overwritten from here on; P and O wait for the PV before
             tc_fence_before_sync();
             arrive(&bars->s_free[u]);
@@ -1330,11 +1341,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               // O is complete up to the block before: S was issued after its PV
               if (rescale && n > 0) scale_o_row<D>(tO, alpha);
             };
-            // unmasked block, every row has a reference: exponentials and
-            // maximum side by side; redone if some row grew by more than 2^8
-            if (full && __all_sync(0xffffffffu, m_use != -INFINITY)) {
+            // every row has a reference: exponentials and maximum side by
+            // side; redone if some row grew by more than 2^8
+            bool done = false;
+            auto guess = [&](auto masked) {
               float s[kBN];
-              load_s(s);
+              load_s(s, masked);
               const float nm = neg_ref();
               const float2 negm = make_float2(nm, nm);
               float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -1350,19 +1362,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 put_p<DT>(pk[c >> 6], pair & 31, pp.x, pp.y);
               }
               const float m_new = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * sl2;
-              if (__any_sync(0xffffffffu, m_new > m_use + kRescaleThreshold)) {
-                float s2[kBN];
-                load_s(s2);
-                exact_pass(s2);
-              } else {
+              done = !__any_sync(0xffffffffu, m_new > m_use + kRescaleThreshold);
+              if (done) {
                 store_p_half<DT>(tP, 0, pk[0]);
                 store_p_half<DT>(tP, 1, pk[1]);
                 ls[0] = lf[0];
                 ls[1] = lf[1];
               }
-            } else {
+            };
+            if (__all_sync(0xffffffffu, m_use != -INFINITY)) {
+              if (k0 >= full_lo && k0 + kBN - 1 <= full_hi)   // (a copy without masks: 5 % of a long prefill)
+                guess(std::false_type{});
+              else
+                guess(std::true_type{});
+            }
+            if (!done) {
               float s[kBN];
-              load_s(s);
+              load_s(s, std::true_type{});
               exact_pass(s);
             }
           }
