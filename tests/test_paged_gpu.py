@@ -373,3 +373,64 @@ def test_given_stream_owns_what_is_allocated():
         assert stream_of(t) == st.cuda_stream
     assert torch.cuda.current_stream() == torch.cuda.default_stream()
     st.synchronize()
+
+
+@pytest.mark.parametrize("H,H_kv,q_lens", [
+    (8, 1, [1, 2, 1]), (4, 2, [4, 5, 3]), (2, 2, [8, 9, 7]), (9, 1, [1, 1, 2]), (6, 1, [1, 260, 2]),
+    (16, 1, [1, 9, 1]),
+])
+@pytest.mark.parametrize("D,wl", [(64, -1), (128, -1), (48, 200), (128, 90)])
+def test_few_rows(H, H_kv, q_lens, D, wl):
+    # up to 8 rows (tokens x heads of a group) four lanes share a row; around it
+    b = Batch(q_lens, [777, 1030, 128], H, H_kv, D, BF16, 16, seed=H + D)
+    b.check(*b.run(window_left=wl), wl=wl)
+
+
+@pytest.mark.parametrize("wl", [-1, 300])
+def test_growing_maxima_wide_heads(wl):
+    # as above for D 128, where a masked block's exponentials are tried against
+    # the old reference first (the products' sums of equal terms are exact)
+    m, D = 1500, 128
+    b = Batch([1, 200, 300], [m, m, 300], 4, 2, D, F16, 16, seed=13)
+    for r, n in enumerate((m, m, 300)):
+        pg = b.table[r, : -(-n // 16)].long()
+        k = b.k[pg].flatten(0, 1)
+        ramp = torch.arange(n, device="cuda").to(torch.float32) / n
+        k[:n] = (ramp[:, None, None] * 2).half()
+        b.k[pg] = k.view(-1, 16, 2, D)
+    b.q.fill_(2.0)       # scores 2 * 2 * ramp * 128 / 11.3 = 45 * ramp
+    b.check(*b.run(window_left=wl), wl=wl)
+
+
+def test_requests_on_many_short_pieces():
+    # decoding, verifying a few tokens and chunks side by side, more items than
+    # blocks of the device: cuts fall on borders, inside items and near their ends
+    g = torch.Generator().manual_seed(3)
+    q = [1, 4, 33, 129, 257, 2, 64] * 30
+    kv = [n + int(x) for n, x in zip(q, torch.randint(0, 900, (len(q),), generator=g))]
+    b = Batch(q, kv, 8, 2, 128, BF16, 16, seed=41)
+    out, lse = b.run()
+    b.check(out, lse)
+    again = b.run()
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
+def test_graphs_and_eager_calls_share_a_workspace_in_turn():
+    b = Batch([1, 300, 5, 1], [9000, 2000, 700, 50], 8, 2, 128, BF16, 16, seed=2)
+    ws = torch.full((fa.fa_paged_workspace_bytes(128),), 255, dtype=torch.uint8, device="cuda")
+    first, first_lse = b.run(workspace=ws)
+    b.check(first, first_lse)
+    args = (b.q, b.k, b.v, b.table, b.cu_q, b.kv_lens)
+    out, lse = torch.empty_like(b.q), torch.empty_like(first_lse)
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for g in graphs:
+        with torch.cuda.graph(g):
+            fa.flash_fwd_paged(*args, out=out, lse=lse, workspace=ws)
+    real = int(b.cu_q[-1])
+    for i in range(6):
+        if i == 3:
+            ws.random_(0, 255)   # what another user of the memory leaves
+        graphs[i % 2].replay()
+        fa.flash_fwd_paged(*args, workspace=ws)
+        torch.cuda.synchronize()
+        assert torch.equal(out[:real], first[:real]) and torch.equal(lse[:real], first_lse[:real])
