@@ -434,3 +434,12 @@ def test_graphs_and_eager_calls_share_a_workspace_in_turn():
         fa.flash_fwd_paged(*args, workspace=ws)
         torch.cuda.synchronize()
         assert torch.equal(out[:real], first[:real]) and torch.equal(lse[:real], first_lse[:real])
+
+
+def test_requests_share_pages():
+    # one prompt's full pages at the head of the others' tables
+    b = Batch([1, 200, 1, 3], [700, 640, 900, 500], 8, 2, 128, BF16, 64, seed=51)
+    for r in (1, 2, 3):
+        b.table[r, :7] = b.table[0, :7]
+    b.check(*b.run())
+    b.check(*b.run(window_left=222), wl=222)
