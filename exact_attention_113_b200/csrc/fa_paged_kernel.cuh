@@ -42,6 +42,14 @@
 // chunks and the latency of an item's ends); one request over 800 tokens, H32/8
 // D128, 16 us (launch, set-up 3, one block's chain 4, joining 5).
 //
+// The weights P enter the product with V in 16 bits, as the tensor cores take
+// them beside a 16-bit V and as in the dense forward; the normaliser sums them
+// unrounded.  Each is off by at most half a step (2^-8 of a bf16 weight, 2^-11 of
+// an fp16 one), which moves O by no more than that share of sum_j p_j |v_j| / l;
+// a second product for what the rounding took off would cost a prefill half as
+// much again.  Up to 8 rows (decoding) have that second product for nothing, see
+// kFewRows (64 requests over 8k: 317 us without, 319 with it).
+//
 // V rows no query of the item sees (behind the request's end, in a page's
 // unwritten tail, or before every window) are cleared in shared memory: their
 // weight is an exact 0, but 0 times an unwritten NaN would not be.
@@ -59,6 +67,9 @@ constexpr int kItemRing = 3;         // items announced ahead
 // matrix fragment: four lanes share a row, 32 of a block's 128 exponentials each.
 // One warp's 128 of a lane had set the pace (128 requests over 500 tokens, H32/8
 // D128: 76 us so, 57 shared; 8 over 1000: 24.5 and 22).
+// The fragment's other 8 rows, idle then, hold what the rounding of the weights
+// to 16 bits took off, so the same products sum it, and the epilogue adds row
+// g + 8 to row g: weights of 16 bits (bf16) or 22 (fp16) of precision.
 constexpr int kFewRows = 8;
 
 struct PagedParams {
@@ -511,6 +522,17 @@ __device__ __forceinline__ void tmem_st_rows16(uint32_t taddr, const uint32_t (&
       "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
+}
+
+// What the rounding of two values to 16 bits took off, itself so rounded.
+template <int DT>
+__device__ __forceinline__ uint32_t pack2_rest(const float2 &x, uint32_t rounded) {
+  float2 r;
+  if constexpr (DT == 0)
+    r = __half22float2(*reinterpret_cast<const __half2 *>(&rounded));
+  else
+    r = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&rounded));
+  return pack2<DT>(x.x - r.x, x.y - r.y);
 }
 
 __device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
@@ -1200,7 +1222,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float2 pp = make_float2(ex2(e.x), ex2(e.y));
             ls[j & 1] = __fadd2_rn(ls[j & 1], pp);
             pk[2 * j] = pack2<DT>(pp.x, pp.y);
-            pk[2 * j + 1] = 0u;
+            pk[2 * j + 1] = pack2_rest<DT>(pp, pk[2 * j]);   // row g + 8
           }
           if (kSplitP && ns > 0) {
             ok = mbar_wait_warp(smem_u32(&bars->pv_done[u]), (ns - 1) & 1, abort_flag);
@@ -1210,7 +1232,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_st_rows16(tP, pk);
           if (kSplitP && n == 0) {   // zeros behind, for the power
 #pragma unroll
-            for (int j = 0; j < 16; ++j) pk[2 * j] = 0u;
+            for (int j = 0; j < 32; ++j) pk[j] = 0u;
             tmem_st_rows16(tP + (16u << 16), pk);
           }
           if (rescale && n > 0)
@@ -1220,7 +1242,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_before_sync();
           arrive(&bars->p_full[u]);
         }
-        // a lane holds the row of its TMEM lane again (the first 8)
+        // a lane holds the row of its TMEM lane again (the first 8, and in the
+        // next 8 the same rows, whose O is the weights' rests')
         l += __shfl_xor_sync(0xffffffffu, l, 1);
         l += __shfl_xor_sync(0xffffffffu, l, 2);
         l = __shfl_sync(0xffffffffu, l, (4 * lane) & 31);
@@ -1462,6 +1485,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               reg_dep(x0);
 #pragma unroll
               for (int v = 0; v < 16; ++v) o[v] = sa * __uint_as_float(x0[v]);
+            }
+            if (few) {
+#pragma unroll
+              for (int v = 0; v < 16; ++v) o[v] += __shfl_down_sync(0xffffffffu, o[v], 8);
             }
           }
           if (valid && t.slot >= 0) {

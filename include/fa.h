@@ -503,6 +503,11 @@ size_t fa_paged_workspace_bytes(int D);
  * Cache rows behind kv_len may hold anything, NaN included; a key or value
  * that some query of a request's 2 * floor(128 / (H / H_kv)) neighbouring
  * tokens sees has to be finite to leave the others' results finite.
+ * Weights: the products and the softmax statistics are fp32.  For the product
+ * with v a weight is rounded to 16 bits, as in fa_fwd, and moves out by at most
+ * half a step (bf16 2^-8, fp16 2^-11) of sum_j p_j |v_j| / l; where a request's
+ * new tokens times H / H_kv are at most 8 (decoding) what the rounding took off is
+ * summed too (2^-16, 2^-22), as fa_fwd's contiguous decoding keeps them in fp32.
  * The results do not depend on timing: the same bits for the same lengths.
  * Lengths live on the device and are not checked on the host: sums that
  * exceed total_q and lengths that exceed max_pages * page_size are cut.
