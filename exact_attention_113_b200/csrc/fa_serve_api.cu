@@ -4,6 +4,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <limits>
 
 #include <cuda_runtime.h>
 
@@ -68,7 +69,10 @@ RopeParams rope_params(const fa_rope_args *a) {
   r.rot = a->rot_dim;
   r.max_pos = a->max_pos;
   r.interleaved = a->interleaved != 0;
-  r.eps = a->eps;
+  // At least the smallest normal number: without it a row of zeros, and the lanes
+  // of a step behind the last head, which hold zeros and are in the weights' sums,
+  // would be 0 times infinity.  It is lost beside any mean square of 2^-102 or more.
+  r.eps = std::max(a->eps, std::numeric_limits<float>::min());
   r.inv_d = 1.0f / a->D;
   return r;
 }

@@ -425,7 +425,7 @@ typedef struct {
     int max_pos;              /* rows of cos_sin */
     int interleaved;          /* pairs (2i, 2i+1); 0: (i, i + rot_dim/2) */
     int dtype;
-    float eps;
+    float eps;                /* >= 0; less than 2^-126 counts as that, so a row of zeros gives zeros */
 } fa_rope_args;
 
 /*
