@@ -67,6 +67,7 @@ __global__ void __launch_bounds__(kPlanThreads) fa_plan_kernel(const PlanParams 
   };
   long long tokens = 0, pages = 0;   // before the tile
   long long missing = 0;             // this thread's requests'
+  const bool counts = blockIdx.x == gridDim.x - 1;   // (the block with the fewest tokens)
   for (int base = 0, tile = 0; base < p.B; base += kPlanTile, ++tile) {
     const int n = min(kPlanTile, p.B - base);
     int q[kEach], ctx[kEach], grown[kEach];
@@ -122,12 +123,19 @@ __global__ void __launch_bounds__(kPlanThreads) fa_plan_kernel(const PlanParams 
         if (base + i == p.B - 1) p.cu_q[p.B] = plan_sat(at + q[e]);
         p.kv_lens[base + i] = plan_sat(static_cast<long long>(ctx[e]) + q[e]);
       }
-      if (blockIdx.x == 0) {
+      if (counts) {
         // new tokens behind the last page the request could get
         const long long got = min(static_cast<long long>(grown[e]), max(p.n_free - first, 0ll));
         const long long room =
             (static_cast<long long>(min(pages_of(ctx[e]), p.max_pages)) + got) * P - ctx[e];
         missing += q[e] - min(static_cast<long long>(q[e]), max(room, 0ll));
+        // and those in the partly filled page that they continue, where an earlier
+        // step got none (its entry is old: no block writes it)
+        const unsigned c = static_cast<unsigned>(ctx[e]), size = static_cast<unsigned>(P);
+        const unsigned in_page = c % size, at_page = c / size;
+        if (in_page != 0 && q[e] > 0 && at_page < static_cast<unsigned>(p.max_pages) &&
+            p.table[(base + i) * p.table_stride + at_page] < 0)
+          missing += min(q[e], P - static_cast<int>(in_page));
       }
       at += q[e];
       first += grown[e];
@@ -162,7 +170,7 @@ __global__ void __launch_bounds__(kPlanThreads) fa_plan_kernel(const PlanParams 
     p.positions[t] = -1;
     p.slots[t] = -1;
   }
-  if (blockIdx.x == 0) {
+  if (counts) {
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) missing += __shfl_xor_sync(0xffffffffu, missing, d);
     if (lane == 0) short_s[warp] = missing;

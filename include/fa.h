@@ -387,7 +387,8 @@ int fa_fwd_splitkv_static(const void *q, const void *k, const void *v, void *out
  *                slot, or -1 (behind the last request, or no page)
  *   counts       device int [3] written: new tokens in all, pages taken,
  *                new tokens without a slot (the free list ran out, whose
- *                table entries get -1, or the table's columns)
+ *                table entries get -1, in this call or an earlier one, or the
+ *                table's columns)
  * num_tokens is the capacity of positions and slots: a padded batch of a
  * captured graph has more than the requests' tokens, and tokens beyond it
  * are not written.  What is written may not overlap anything else (the next
