@@ -100,16 +100,22 @@ struct PagedParams {
 // ------------------------------------------------------------------ the work line
 struct PagedReq {
   int q_start, q_len, kv_len;
+  int first;   // position of the first new token
 };
 
-// Lengths of request b, clamped to the tensors: bad lengths give wrong rows,
-// never an access outside them.
+// Lengths of request b, cut to the tensors: no access lies outside them, and
+// the tokens that have a row keep their positions.  (kv_lens and cu_q may hold
+// anything; a position is at most 2^30 from 0 with all tokens of the request, so
+// that sums with a window stay ints.)
 __device__ __forceinline__ PagedReq paged_req(const PagedParams &p, int b) {
   PagedReq r;
   const int a = __ldg(p.cu_q + b), e = __ldg(p.cu_q + b + 1);
   r.q_start = min(max(a, 0), p.total_q);
   r.q_len = max(min(e, p.total_q) - r.q_start, 0);
-  r.kv_len = min(max(__ldg(p.kv_lens + b), 0), p.max_kv);
+  const int kv = max(__ldg(p.kv_lens + b), 0);
+  r.kv_len = min(kv, p.max_kv);
+  const long long first = static_cast<long long>(kv) - e + r.q_start;
+  r.first = static_cast<int>(max(min(first, (1ll << 30) - r.q_len), -(1ll << 30)));
   return r;
 }
 
@@ -120,7 +126,7 @@ __device__ __forceinline__ int paged_pairs(const PagedParams &p, int q_len) {
 // Keys [klo, khi] that tokens [i0, i0 + n) of the request see; khi < klo: none.
 __device__ __forceinline__ void paged_keys(const PagedParams &p, const PagedReq &r, int i0, int n,
                                            int &klo, int &khi) {
-  const int first = r.kv_len - r.q_len + i0, last = first + n - 1;
+  const int first = r.first + i0, last = first + n - 1;
   klo = p.wl < 0 ? 0 : max(0, first - p.wl);
   khi = p.wr < 0 ? r.kv_len - 1 : min(r.kv_len - 1, last + p.wr);
   if (n <= 0 || khi < klo) {
@@ -178,6 +184,7 @@ __device__ __forceinline__ long long paged_head_cost(const PagedParams &p, const
     o.q_start = 0;
     o.q_len = __shfl_sync(0xffffffffu, r.q_len, src);
     o.kv_len = __shfl_sync(0xffffffffu, r.kv_len, src);
+    o.first = __shfl_sync(0xffffffffu, r.first, src);
     const int n = paged_pairs(p, o.q_len);
     long long all = 0;
     for (int i = lane; i < n; i += 32) all += paged_cost(p, o, i).cost;
@@ -236,7 +243,7 @@ __device__ __forceinline__ void paged_find_piece(const PagedParams &p, PagedSetu
   constexpr int kWarps = kThreads / 32;
   auto cost_of = [&](int b) {
     PagedReq r;
-    r.q_start = r.q_len = r.kv_len = 0;
+    r.q_start = r.q_len = r.kv_len = r.first = 0;
     if (b < p.B) r = paged_req(p, b);
     return paged_head_cost(p, r);
   };
@@ -386,7 +393,7 @@ struct PagedWalk {
     t.tok0 = r.q_start + i0;
     t.nt0 = min(p.tile_q, r.q_len - i0);
     t.nt1 = min(p.tile_q, r.q_len - i0 - t.nt0);
-    t.first = r.kv_len - r.q_len + i0;
+    t.first = r.first + i0;
     t.kv_len = r.kv_len;
     t.once = r.q_len <= 2 * p.tile_q;
     int klo0, khi0, klo1 = 0, khi1 = -1;
@@ -1155,9 +1162,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool busy = __any_sync(0xffffffffu, valid);
       const bool few = single && nt * p.group <= kFewRows;
       const int x = first + (few ? few_tok : r_tok);   // this lane's row of the softmax
-      const int row_lo = p.wl < 0 ? 0 : x - p.wl;
+      const int row_lo = p.wl < 0 ? 0 : max(0, x - p.wl);
       const int row_hi = p.wr < 0 ? t.kv_len - 1 : min(t.kv_len - 1, x + p.wr);
-      const int full_lo = p.wl < 0 ? 0 : last - p.wl;
+      const int full_lo = p.wl < 0 ? 0 : max(0, last - p.wl);
       const int full_hi = p.wr < 0 ? t.kv_len - 1 : min(t.kv_len - 1, first + p.wr);
       const int j0 = single ? t.lo + u : (tile ? t.lo1 : t.lo0);
       const int jstep = single ? 2 : 1;

@@ -510,8 +510,9 @@ size_t fa_paged_workspace_bytes(int D);
  * new tokens times H / H_kv are at most 8 (decoding) what the rounding took off is
  * summed too (2^-16, 2^-22), as fa_fwd's contiguous decoding keeps them in fp32.
  * The results do not depend on timing: the same bits for the same lengths.
- * Lengths live on the device and are not checked on the host: sums that
- * exceed total_q and lengths that exceed max_pages * page_size are cut.
+ * Lengths live on the device and are not checked on the host.  New tokens
+ * behind total_q have no rows and tokens behind max_pages * page_size no keys;
+ * the others keep their positions (kv_len - q_len + i with the lengths given).
  * total_q == 0 is a no-op.  Other errors as fa_fwd.
  */
 int fa_fwd_paged(const void *q, long long q_stride_t, long long q_stride_h, const void *k_cache,

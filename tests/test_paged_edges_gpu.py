@@ -1,4 +1,5 @@
-"""fa_fwd_paged: how exact the weights of a decoding tile are, against float64."""
+"""fa_fwd_paged: how exact the weights of a decoding tile are, and requests that
+the tensors cut; against float64."""
 from __future__ import annotations
 
 import math
@@ -12,6 +13,7 @@ from tests.test_paged_gpu import Batch
 
 pytestmark = pytest.mark.gpu
 F16, BF16 = torch.float16, torch.bfloat16
+SEEN = 1 / math.sqrt(64)
 
 
 def _exact_weights_bound(out, mag, total, dtype):
@@ -52,3 +54,54 @@ def test_weights_of_one_request_cut_over_all_ctas():
     want, _, mag, total = ref.attention(b.q, *clean, b.table, b.cu_q, b.kv_lens, 1 / math.sqrt(128),
                                         True, -1, -1)
     assert ((out.double() - want).abs() <= _exact_weights_bound(want, mag, total, BF16))[:1].all()
+
+
+# ------------------------------------------------------------ cut requests
+def _close(out, lse, want, dtype):
+    o, e, mag, total = want
+    assert ((out.double() - o).abs() <= ref.attention_bound(o, mag, total, dtype)).all()
+    seen = torch.isfinite(e)
+    assert torch.equal(torch.isneginf(lse), ~seen)
+    assert ((lse.double() - e)[seen].abs() <= ref.LSE_BOUND).all()
+
+
+@pytest.mark.parametrize("wl", [-1, 70])
+@pytest.mark.parametrize("rows", [50, 73, 3, 330])
+def test_rows_of_a_request_that_total_q_cuts(rows, wl):
+    # the last request's new tokens do not all have a row: those that have one
+    # keep their places, and see no key behind them
+    b = Batch([2, 40, 300], [90, 40, 700], 4, 2, 64, F16, 16, seed=60, pad_rows=0)
+    clean = [torch.nan_to_num(c, nan=0.0) for c in (b.k, b.v)]
+    want = ref.attention(b.q, *clean, b.table, b.cu_q, b.kv_lens, SEEN, True, wl, -1)
+    out, lse = fa.flash_fwd_paged(b.q[:rows], b.k, b.v, b.table, b.cu_q, b.kv_lens, window_left=wl)
+    _close(out, lse, [t[:rows] for t in want], F16)
+
+
+def test_keys_behind_a_table_that_is_too_narrow():
+    # positions 100 .. 199 over a table of 128 tokens: the keys that it holds,
+    # each token at its own place
+    b = Batch([100], [200], 4, 2, 64, BF16, 16, seed=61, pad_rows=0)
+    clean = [torch.nan_to_num(c, nan=0.0) for c in (b.k, b.v)]
+    out, lse = fa.flash_fwd_paged(b.q, b.k, b.v, b.table[:, :8].clone(), b.cu_q, b.kv_lens)
+
+    def part(rows, kv, causal):
+        q = b.q[rows]
+        cu = torch.tensor([0, q.shape[0]], dtype=torch.int32, device="cuda")
+        n = torch.tensor([kv], dtype=torch.int32, device="cuda")
+        return ref.attention(q, *clean, b.table, cu, n, SEEN, causal, -1, -1)
+    _close(out[:28], lse[:28], part(slice(0, 28), 128, True), BF16)
+    _close(out[28:], lse[28:], part(slice(28, 100), 128, False), BF16)
+
+
+def test_step_over_its_capacity():
+    # page tables for more tokens than the batch has rows, then the attention
+    lens, ctx, page, T, H, H_kv, D = [30, 50, 60], [10, 100, 7], 16, 100, 4, 2, 64
+    full = Batch(lens, [a + c for a, c in zip(lens, ctx)], H, H_kv, D, BF16, page, seed=62, pad_rows=0)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    p = fa.paged_plan(torch.tensor(lens, **i32), torch.tensor(ctx, **i32), full.table.clone(),
+                      torch.arange(40, **i32), page, T)
+    assert p.cu_q.tolist() == [0, 30, 80, 140] and p.positions.tolist()[80:] == list(range(7, 27))
+    out, lse = fa.flash_fwd_paged(full.q[:T], full.k, full.v, full.table, p.cu_q, p.kv_lens)
+    clean = [torch.nan_to_num(c, nan=0.0) for c in (full.k, full.v)]
+    want = ref.attention(full.q, *clean, full.table, full.cu_q, full.kv_lens, SEEN, True, -1, -1)
+    _close(out, lse, [t[:T] for t in want], BF16)
