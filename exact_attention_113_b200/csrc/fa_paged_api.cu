@@ -36,6 +36,9 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t
                                   const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
+// So that a walk over requests without new tokens ends within the waits' limit.
+constexpr int kMaxRequests = 1 << 24;
+
 EncodeTiledFn encode_fn() {
   static EncodeTiledFn fn = nullptr;
   static std::once_flag once;
@@ -147,7 +150,8 @@ extern "C" int fa_fwd_paged(const void *q, long long q_stride_t, long long q_str
   if (total_q < 0 || B < 1 || H < 1 || H_kv < 1 || num_pages < 1 || max_pages < 1)
     return FA_ERR_SHAPE;
   if (H % H_kv != 0 || H / H_kv > kBM) return FA_ERR_SHAPE;
-  if (total_q > kMaxLen || static_cast<long long>(B) * H_kv > kMaxLen) return FA_ERR_SHAPE;
+  if (total_q > kMaxLen || B > kMaxRequests || static_cast<long long>(B) * H_kv > kMaxLen)
+    return FA_ERR_SHAPE;
   if (!head_dim_ok(D)) return FA_ERR_HEADDIM;
   if (dtype != FA_F16 && dtype != FA_BF16) return FA_ERR_DTYPE;
   if (page_size < 16 || page_size > kMaxLen || (page_size & (page_size - 1)) != 0)

@@ -371,16 +371,39 @@ struct PagedWalk {
     u = cuts.at(blockIdx.x);
     locate(p, st, 0, u);
   }
+  // To the next item, if the piece has one.  Requests without new tokens (most of
+  // a batch captured for more) are passed over 128 at a time, all lanes looking:
+  // 2^24 of them in some 100 ms, well within the limit of the others' waits.
   __device__ __forceinline__ void advance(const PagedParams &p) {
     off = 0;
+    if (u >= end) return;
     if (++pair < paged_pairs(p, r.q_len)) return;
     pair = 0;
     if (++h < p.H_kv) return;
     h = 0;
-    while (++b < p.B) {
-      r = paged_req(p, b);
-      if (r.q_len > 0) return;
+    if (++b >= p.B) return;
+    r = paged_req(p, b);
+    if (r.q_len > 0) return;
+    constexpr int kLook = 4;
+    const int lane = threadIdx.x & 31;
+    for (++b; b < p.B; b += 32 * kLook) {
+      bool some[kLook];
+#pragma unroll
+      for (int v = 0; v < kLook; ++v) {
+        const int i = b + 32 * v + lane;
+        some[v] = i < p.B && paged_req(p, i).q_len > 0;
+      }
+#pragma unroll
+      for (int v = 0; v < kLook; ++v) {
+        const unsigned hit = __ballot_sync(0xffffffffu, some[v]);
+        if (hit) {
+          b += 32 * v + __ffs(hit) - 1;
+          r = paged_req(p, b);
+          return;
+        }
+      }
     }
+    b = p.B;
   }
   __device__ __forceinline__ bool next(const PagedParams &p, PagedItem &t) {
     if (u >= end || b >= p.B) {

@@ -495,6 +495,8 @@ size_t fa_paged_workspace_bytes(int D);
  *             visible iff j < kv_len, j <= position + window_right (0 when
  *             causal), j >= position - window_left
  *   D         a multiple of 16 in [16, 128]; H / H_kv at most 128
+ *   B         at most 2^24; requests without new tokens (the rest of a captured
+ *             batch) are skipped
  *   page_size a power of two, at least 16 (FA_ERR_ARG)
  *   workspace device, 256-byte aligned, at least fa_paged_workspace_bytes(D)
  *             bytes; contents on entry do not matter.  Calls that share a

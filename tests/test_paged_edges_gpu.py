@@ -1,5 +1,5 @@
-"""fa_fwd_paged: how exact the weights of a decoding tile are, and requests that
-the tensors cut; against float64."""
+"""fa_fwd_paged: how exact the weights of a decoding tile are, requests that the
+tensors cut, against float64; and batches that are mostly empty."""
 from __future__ import annotations
 
 import math
@@ -105,3 +105,30 @@ def test_step_over_its_capacity():
     clean = [torch.nan_to_num(c, nan=0.0) for c in (full.k, full.v)]
     want = ref.attention(full.q, *clean, full.table, full.cu_q, full.kv_lens, SEEN, True, -1, -1)
     _close(out, lse, [t[:T] for t in want], BF16)
+
+
+# ------------------------------------------------------------ empty requests
+@pytest.mark.parametrize("n,B,kind", [
+    (8, 512, "behind"), (8, 512, "before"), (8, 600, "spread"), (300, 5000, "spread"),
+    (1, 4000, "between"), (300, 1 << 20, "spread"), (2, 1 << 20, "behind"),
+])
+def test_mostly_empty_batches(n, B, kind):
+    # the same bits as the requests alone: the work is cut in the same places
+    g = torch.Generator().manual_seed(n)
+    q = torch.randint(1, 20, (n,), generator=g).tolist()
+    kv = [x + int(y) for x, y in zip(q, torch.randint(0, 300, (n,), generator=g))]
+    b = Batch(q, kv, 4, 2, 64, F16, 16, seed=70)
+    want = b.run()
+    at = {"behind": torch.arange(n), "before": torch.arange(B - n, B),
+          "between": torch.full((n,), B // 2),
+          "spread": torch.linspace(0, B - 1, n).long()}[kind]
+    lens = torch.zeros(B, dtype=torch.int32)
+    lens[at] = torch.tensor(q, dtype=torch.int32)
+    kvs = torch.full((B,), 33, dtype=torch.int32)       # empty requests may have a cache
+    kvs[at] = b.kv_lens.cpu()
+    table = torch.full((B, b.table.shape[1]), -1, dtype=torch.int32, device="cuda")
+    table[at.cuda()] = b.table
+    b.cu_q = torch.cat([torch.zeros(1, dtype=torch.int32), lens.cumsum(0).int()]).cuda()
+    b.kv_lens, b.table = kvs.cuda(), table
+    got = b.run()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
