@@ -540,6 +540,15 @@ __device__ __forceinline__ void tmem_ld_rows16(uint32_t taddr, uint32_t (&r)[32]
       : "r"(taddr)
       : "memory");
 }
+// 16 columns.
+__device__ __forceinline__ void tmem_ld_rows16(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7])
+      : "r"(taddr)
+      : "memory");
+}
 __device__ __forceinline__ void tmem_st_rows16(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.16x128b.x16.b32 [%0], "
@@ -562,7 +571,8 @@ __device__ __forceinline__ uint32_t pack2_rest(const float2 &x, uint32_t rounded
     r = __half22float2(*reinterpret_cast<const __half2 *>(&rounded));
   else
     r = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&rounded));
-  return pack2<DT>(x.x - r.x, x.y - r.y);
+  r = __ffma2_rn(r, make_float2(-1.0f, -1.0f), x);
+  return pack2<DT>(r.x, r.y);
 }
 
 __device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
@@ -607,6 +617,65 @@ __device__ __forceinline__ void paged_store16(const PagedParams &p, uint8_t *oro
   } else {
     *reinterpret_cast<uint4 *>(orow + 2 * c) = make_uint4(w[0], w[1], w[2], w[3]);
     *reinterpret_cast<uint4 *>(orow + 2 * c + 16) = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
+// The results of up to kFewRows rows: a lane takes row g = lane / 4 of TMEM and
+// row g + 8, the same columns of what the weights' rounding took off, so that
+// their sum needs no exchange (64 requests over 1000, H32/8 D128: 59.2 us with rows
+// in lanes and shuffles, so 56.0; before there were rests to add, 56.4).  As in the
+// general epilogue a warpgroup joins every other 16 columns of the two O; sa, sb:
+// their factors, of row `lane`.
+template <int D, int DT>
+__device__ __forceinline__ void paged_few_rows(const PagedParams &p, const PagedItem &t,
+                                               uint32_t from, int u, int tok_of_g, bool none,
+                                               bool two, float sa, float sb, int slot) {
+  constexpr int kChunks = (D + 31) / 32;
+  const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  const float ga = __shfl_sync(0xffffffffu, sa, g), gb = __shfl_sync(0xffffffffu, sb, g);
+  float2 o[kChunks][2];   // columns c + 2q, c + 2q + 1 and c + 8 + 2q, c + 9 + 2q
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i) o[i][0] = o[i][1] = make_float2(0.0f, 0.0f);
+  auto held = [&](int i) { return 32 * i + 16 < D || u == 0; };
+  auto add = [&](uint32_t at, float w) {
+    uint32_t x[kChunks][8];
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i)
+      if (held(i)) tmem_ld_rows16(at + 32 * i, x[i]);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+      reg_dep(x[i]);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t *v = x[i] + 4 * e;
+        o[i][e].x += w * (__uint_as_float(v[0]) + __uint_as_float(v[2]));
+        o[i][e].y += w * (__uint_as_float(v[1]) + __uint_as_float(v[3]));
+      }
+    }
+  };
+  if (!none) add(from + 16 * u, ga);
+  if (two) add(from + D + 16 * u, gb);
+  if (tok_of_g >= t.nt0) return;
+  if (t.slot >= 0) {
+    float2 *at = reinterpret_cast<float2 *>(paged_slot(p, D, slot) + g) + (q & 1);
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i)
+      if (held(i))
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          at[2 * (4 * (2 * i + u) + 2 * e + (q >> 1)) * kPagedRows] = o[i][e];
+  } else {
+    const int head = t.h * p.group + g - tok_of_g * p.group;
+    uint8_t *at = static_cast<uint8_t *>(p.out) +
+                  2 * (static_cast<long long>(t.tok0 + tok_of_g) * p.out_st +
+                       static_cast<long long>(head) * p.out_sh + 16 * u + 2 * q);
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i)
+      if (held(i))
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          *reinterpret_cast<uint32_t *>(at + 64 * i + 16 * e) = pack2<DT>(o[i][e].x, o[i][e].y);
   }
 }
 
@@ -1492,8 +1561,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         float4 *wo = paged_slot(p, D, slot) + srow;
         const uint32_t from = single ? tO0 : tO;
         const float sa = wa * inv, sb = wb * inv;
+        if (few)
+          paged_few_rows<D, DT>(p, t, tO0, u, few_tok, none, two, sa, sb, slot);
 #pragma unroll 1
-        for (int c = single ? 16 * u : 0; c < D; c += single ? 32 : 16) {
+        for (int c = few ? D : (single ? 16 * u : 0); c < D; c += single ? 32 : 16) {
           float o[16];
           if (none) {
 #pragma unroll
@@ -1515,10 +1586,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               reg_dep(x0);
 #pragma unroll
               for (int v = 0; v < 16; ++v) o[v] = sa * __uint_as_float(x0[v]);
-            }
-            if (few) {
-#pragma unroll
-              for (int v = 0; v < 16; ++v) o[v] += __shfl_down_sync(0xffffffffu, o[v], 8);
             }
           }
           if (valid && t.slot >= 0) {
