@@ -40,20 +40,23 @@ int rope_tensor(const fa_rope_args *a, const fa_rows &t, int heads, bool needed)
   return FA_OK;
 }
 
-RopeView view(const fa_rows &t) {
+// A tensor as the kernels walk it.  The stride of a one-element axis may be any
+// number; lanes behind the last head form addresses with it, which a copy of no
+// bytes wants aligned too, so it becomes 0.
+RopeView view(const fa_rope_args *a, const fa_rows &t, int heads) {
   RopeView v;
   v.ptr = static_cast<const uint8_t *>(t.ptr);
-  v.sb = t.stride_b;
-  v.sl = t.stride_l;
-  v.sh = t.stride_h;
+  v.sb = a->B > 1 ? t.stride_b : 0;
+  v.sl = a->L > 1 ? t.stride_l : 0;
+  v.sh = heads > 1 ? t.stride_h : 0;
   return v;
 }
 
 RopeParams rope_params(const fa_rope_args *a) {
   RopeParams r;
   std::memset(&r, 0, sizeof(r));
-  r.q = view(a->q);
-  r.k = view(a->k);
+  r.q = view(a, a->q, a->H);
+  r.k = view(a, a->k, a->H_kv);
   r.wq = a->q_weight;
   r.wk = a->k_weight;
   r.cos_sin = a->cos_sin;
@@ -237,10 +240,10 @@ extern "C" int fa_qk_norm_rope(const fa_rope_args *a, cudaStream_t stream) {
       !al(a->k_weight, 16))
     return FA_ERR_ALIGN;
   RopeParams r = rope_params(a);
-  r.qo = view(a->q_out);
-  r.ko = view(a->k_out);
+  r.qo = view(a, a->q_out, a->H);
+  r.ko = view(a, a->k_out, a->H_kv);
   if (cache) {
-    r.v = view(a->v);
+    r.v = view(a, a->v, a->H_kv);
     r.kc = static_cast<uint8_t *>(a->k_cache);
     r.vc = static_cast<uint8_t *>(a->v_cache);
     r.c_sp = a->cache_stride_page;
@@ -297,10 +300,10 @@ extern "C" int fa_qk_norm_rope_bwd(const fa_rope_args *a, fa_rows dq, fa_rows dk
       !al(a->k_weight, 16))
     return FA_ERR_ALIGN;
   RopeParams r = rope_params(a);
-  r.dyq = view(a->q_out);
-  r.dyk = view(a->k_out);
-  r.dq = view(dq);
-  r.dk = view(dk);
+  r.dyq = view(a, a->q_out, a->H);
+  r.dyk = view(a, a->k_out, a->H_kv);
+  r.dq = view(a, dq, a->H);
+  r.dk = view(a, dk, a->H_kv);
   r.dwq = dq_weight;
   r.dwk = dk_weight;
   if (dq_weight || dk_weight) {

@@ -132,3 +132,16 @@ def test_mostly_empty_batches(n, B, kind):
     b.kv_lens, b.table = kvs.cuda(), table
     got = b.run()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_strides_of_one_element_axes():
+    # one token, one head, one K/V head, one page
+    for H, H_kv, T, kv in ((8, 2, 1, 300), (1, 1, 5, 200), (4, 1, 1, 9)):
+        b = Batch([T], [kv], H, H_kv, 64, BF16, 256 if H == 4 else 16, seed=80, pad_rows=0)
+        want, want_lse = b.run()
+
+        def odd(x):
+            return x.as_strided(x.shape, [n if x.shape[a] > 1 else 3 for a, n in enumerate(x.stride())])
+        out = odd(torch.full_like(b.q, 3.0))
+        _, lse = fa.flash_fwd_paged(odd(b.q), odd(b.k), odd(b.v), b.table, b.cu_q, b.kv_lens, out=out)
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)

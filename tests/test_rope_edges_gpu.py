@@ -1,4 +1,5 @@
-"""fa_qk_norm_rope and its gradient without an epsilon, against float64."""
+"""fa_qk_norm_rope and its gradient without an epsilon, and with axes of one
+element, against float64."""
 from __future__ import annotations
 
 import pytest
@@ -70,3 +71,33 @@ def test_rows_of_zeros_without_an_epsilon():
     _rows_ok(qo[keep], q[keep], wq, cs, pos[keep], False, 0.0)
     got = fa.qk_norm_rope_bwd(q, k, wq, wk, cs, pos, torch.zeros_like(q), k, eps=0.0)
     assert (got[0] == 0).all() and (got[2] == 0).all()
+
+
+# ------------------------------------------------------------ axes of one element
+def _odd(x, axes):
+    """x with strides of 3 elements along its one-element axes."""
+    for a in axes:
+        assert x.shape[a] == 1
+    stride = [3 if a in axes else n for a, n in enumerate(x.stride())]
+    return x.as_strided(x.shape, stride, x.storage_offset())
+
+
+@pytest.mark.parametrize("D", [16, 64, 128])
+@pytest.mark.parametrize("shape,H,H_kv,axes", [((50,), 1, 1, (1,)), ((1, 1), 6, 2, (0, 1)),
+                                               ((1, 40), 1, 1, (0, 2))])
+def test_strides_of_one_element_axes(D, shape, H, H_kv, axes):
+    q, k, v, wq, wk, cs, pos = _inputs(shape, H, H_kv, D, D, BF16, seed=D)
+    q, k, v = (_odd(x.contiguous(), axes) for x in (q, k, v))
+    qo, ko = (_odd(torch.full(x.shape, 5.0, dtype=BF16, device="cuda"), axes) for x in (q, k))
+    T = pos.numel()
+    cache = [torch.full((T // 16 + 1, 16, H_kv, D), 7.0, dtype=BF16, device="cuda") for _ in range(2)]
+    fa.qk_norm_rope(q, k, wq, wk, cs, pos, eps=EPS, q_out=qo, k_out=ko, v=v, k_cache=cache[0],
+                    v_cache=cache[1], slots=torch.arange(T, device="cuda"))
+    _rows_ok(qo, q, wq, cs, pos, False)
+    _rows_ok(ko, k, wk, cs, pos, False)
+    assert torch.equal(cache[0].flatten(0, 1)[:T], ko.reshape(T, H_kv, D))
+    assert torch.equal(cache[1].flatten(0, 1)[:T], v.reshape(T, H_kv, D))
+    dyq, dyk = _odd(q.clone(), axes), _odd(k.clone(), axes)
+    got = fa.qk_norm_rope_bwd(q, k, wq, wk, cs, pos, dyq, dyk, eps=EPS,
+                              dq=_odd(torch.empty_like(q.contiguous()), axes))
+    _backward_ok(q, k, wq, wk, cs, pos, dyq, dyk, got, False, EPS)
