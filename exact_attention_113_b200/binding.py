@@ -374,6 +374,14 @@ def fa_version() -> int:
 
 
 # ------------------------------------------------------------ torch call
+def _workspace(t):
+    """(pointer, bytes) of a given or allocated workspace; its size is taken
+    from its elements, which have to lie in it."""
+    if not t.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return t.data_ptr(), t.numel()
+
+
 def flash_fwd(q, k, v, scale=None, causal=False, window_left=-1, window_right=-1,
               return_lse=True, out=None, lse=None, stream=None, n_splits=0,
               workspace=None, mask=None, return_softmax_stats=False):
@@ -468,8 +476,8 @@ def flash_fwd(q, k, v, scale=None, causal=False, window_left=-1, window_right=-1
             st = fa_fwd_splitkv(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
                                 lse.data_ptr() if lse is not None else None,
                                 B, H, H_kv, L_q, L_k, D, scale, causal, window_left,
-                                window_right, dtype, n_splits, workspace.data_ptr(),
-                                workspace.numel(), stream.cuda_stream)
+                                window_right, dtype, n_splits, *_workspace(workspace),
+                                stream.cuda_stream)
             where = "fa_fwd_splitkv"
     if st != FA_OK:
         raise FaError(st, where)
@@ -516,8 +524,7 @@ def flash_bwd(q, k, v, out, dout, lse, scale=None, causal=False, window_left=-1,
             st = fa_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
                         dout.data_ptr(), lse.data_ptr(), dq.data_ptr(), dk.data_ptr(),
                         dv.data_ptr(), B, H, H_kv, L_q, L_k, D, scale, causal, window_left,
-                        window_right, dtype, workspace.data_ptr(), workspace.numel(),
-                        stream.cuda_stream)
+                        window_right, dtype, *_workspace(workspace), stream.cuda_stream)
             where = "fa_bwd"
         else:
             if not mask.is_cuda or mask.device != q.device:
@@ -527,7 +534,7 @@ def flash_bwd(q, k, v, out, dout, lse, scale=None, causal=False, window_left=-1,
                            dout.data_ptr(), lse.data_ptr(), dq.data_ptr(), dk.data_ptr(),
                            dv.data_ptr(), mask.data_ptr(), mtype, sb, sh, sq, B, H, H_kv, L_q,
                            L_k, D, scale, causal, window_left, window_right, dtype,
-                           workspace.data_ptr(), workspace.numel(), stream.cuda_stream)
+                           *_workspace(workspace), stream.cuda_stream)
             where = "fa_bwd_ex"
     if st != FA_OK:
         raise FaError(st, where)
@@ -604,8 +611,8 @@ def flash_fwd_fp8(q, k, v, scale=None, descale_q=1.0, descale_k=1.0, descale_v=1
             st = fa_fwd_fp8_splitkv(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
                                     lse.data_ptr() if lse is not None else None, B, H, H_kv,
                                     L_q, L_k, D, scale, descale_q, descale_k, descale_v, causal,
-                                    window_left, window_right, n_splits, workspace.data_ptr(),
-                                    workspace.numel(), stream.cuda_stream)
+                                    window_left, window_right, n_splits, *_workspace(workspace),
+                                    stream.cuda_stream)
             where = "fa_fwd_fp8_splitkv"
     if st != FA_OK:
         raise FaError(st, where)
@@ -646,7 +653,7 @@ def flash_fwd_host(q, k, v, scale=None, causal=False, window_left=-1, window_rig
     with torch.cuda.device(dev):
         st = fa_fwd_host(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
                          lse.data_ptr(), B, H, H_kv, L_q, L_k, D, scale, causal, window_left,
-                         window_right, dtype, workspace.data_ptr(), workspace.numel(), n_chunks,
+                         window_right, dtype, *_workspace(workspace), n_chunks,
                          stream.cuda_stream)
     if st != FA_OK:
         raise FaError(st, "fa_fwd_host")

@@ -111,6 +111,11 @@ void vec(const at::Tensor *t, const char *name, at::ScalarType type, int64_t n) 
     bad("%s must be a contiguous vector of the right type and length", name);
 }
 
+// A workspace's size is taken from its elements, which have to lie in it.
+void workspace(const at::Tensor *t) {
+  if (t && !t->is_contiguous()) bad("%s must be contiguous", "workspace");
+}
+
 int dtype_of(const at::Tensor *q) {
   if (q->scalar_type() == at::kHalf) return FA_F16;
   if (q->scalar_type() == at::kBFloat16) return FA_BF16;
@@ -355,6 +360,7 @@ PyObject *qk_norm_rope_bwd(PyObject *, PyObject *const *a, Py_ssize_t na) {
                    *dqo = tensor(a[6], "dq_out"), *dko = tensor(a[7], "dk_out"),
                    *dq = tensor(a[10], "dq", true), *dk = tensor(a[11], "dk", true),
                    *ws = tensor(a[12], "workspace", true);
+  workspace(ws);
   fa_rope_args r = rope_common(q, k, wq, wk, cs, pos, real(a[8]), truth(a[9]));
   const at::ScalarType type = q->scalar_type();
   r.q_out = rows_of(dqo, "dq_out", q->sizes(), type);
@@ -411,6 +417,7 @@ PyObject *flash_fwd_paged(PyObject *, PyObject *const *a, Py_ssize_t na) {
                    *table = tensor(a[3], "block_table"), *cu = tensor(a[4], "cu_q"),
                    *kv = tensor(a[5], "kv_lens"), *out = tensor(a[11], "out", true),
                    *lse = tensor(a[12], "lse", true), *ws = tensor(a[13], "workspace", true);
+  workspace(ws);
   if (q->dim() != 3 || q->stride(2) != 1) bad("%sq must be [total_q, H, D], contiguous along D");
   const int T = size32(q->size(0), "q"), H = size32(q->size(1), "q"), D = size32(q->size(2), "q");
   const int dtype = dtype_of(q);
