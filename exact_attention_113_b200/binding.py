@@ -664,7 +664,6 @@ def flash_fwd_host(q, k, v, scale=None, causal=False, window_left=-1, window_rig
 # These run for every layer of a decoding step, where a call's host time
 # counts: their checks and allocations are compiled (csrc/fa_torch.cpp).  With
 # a ``stream`` the call runs and allocates there, else on the current stream.
-EXT_PATH = os.path.join(PKG, "lib", "_fa_torch.so")
 _ext = None
 
 
@@ -674,13 +673,14 @@ def _serving():
     load()
     with _lock:
         if _ext is None:
-            import torch  # noqa: F401  (its libraries, before the module that needs them)
-            if not os.path.exists(EXT_PATH):
+            from .build import binding_path
+            path = binding_path()   # (imports torch, whose libraries the module needs)
+            if not os.path.exists(path):
                 raise RuntimeError(
-                    f"_fa_torch.so not found at {EXT_PATH}; build it with "
-                    "`python -m exact_attention_113_b200.build`")
-            loader = importlib.machinery.ExtensionFileLoader("_fa_torch", EXT_PATH)
-            spec = importlib.util.spec_from_file_location("_fa_torch", EXT_PATH, loader=loader)
+                    f"the torch binding of this torch and Python was not found at {path}; "
+                    "build it with `python -m exact_attention_113_b200.build`")
+            loader = importlib.machinery.ExtensionFileLoader("_fa_torch", path)
+            spec = importlib.util.spec_from_file_location("_fa_torch", path, loader=loader)
             ext = importlib.util.module_from_spec(spec)
             loader.exec_module(ext)
             ext.set_error(FaError)

@@ -14,6 +14,7 @@ import os
 import re
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -109,21 +110,34 @@ TESTHOOKS_FLAGS = ["-DFA_TEST_HOOKS", "-DFA_WAIT_LIMIT_NS=10000000ull"]
 
 # The compiled torch binding of the serving entries: plain C++ against torch's
 # headers, linked to libfa.so beside it; torch's own libraries are in the
-# process before it is imported.
+# process before it is imported.  It is bound to the torch and the Python that
+# it was compiled against, so both are in its name: another torch does not load
+# it, and has its own built.
 BINDING_SOURCE = os.path.join(CSRC, "fa_torch.cpp")
-BINDING_PATH = os.path.join(LIB_DIR, "_fa_torch.so")
 
 
-def build_binding(force: bool = False, verbose: bool = False) -> str:
+def binding_path() -> str:
+    import torch
+    return os.path.join(LIB_DIR, f"_fa_torch.torch-{torch.__version__}"
+                                 f"{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
+def build_binding(force: bool = False, verbose: bool = False) -> str | None:
+    """Path of the binding; None where there is no torch to bind to (the C
+    library does not need it)."""
+    try:
+        path = binding_path()
+    except ImportError:
+        sys.stderr.write("no torch: libfa.so without its torch binding\n")
+        return None
     depends = [BINDING_SOURCE, os.path.join(INCLUDE, "fa.h")]
-    if not force and os.path.exists(BINDING_PATH) and \
-            all(os.path.getmtime(p) <= os.path.getmtime(BINDING_PATH) for p in depends):
-        return BINDING_PATH
-    import sysconfig
+    if not force and os.path.exists(path) and \
+            all(os.path.getmtime(p) <= os.path.getmtime(path) for p in depends):
+        return path
     import torch
     from torch.utils import cpp_extension
     cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
-    tmp = BINDING_PATH + f".tmp{os.getpid()}"
+    tmp = path + f".tmp{os.getpid()}"
     dirs = cpp_extension.include_paths() + [sysconfig.get_paths()["include"],
                                             os.path.join(cuda, "include"), INCLUDE]
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
@@ -135,9 +149,9 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
     if res.returncode != 0 or verbose:
         sys.stderr.write(res.stdout + res.stderr)
     if res.returncode != 0:
-        raise RuntimeError("g++ failed building _fa_torch.so")
-    os.replace(tmp, BINDING_PATH)
-    return BINDING_PATH
+        raise RuntimeError("g++ failed building the torch binding")
+    os.replace(tmp, path)
+    return path
 
 
 def build(force: bool = False, verbose: bool = False, testhooks: bool = False) -> str:
