@@ -1,5 +1,5 @@
-"""fa_qk_norm_rope and its gradient without an epsilon, and with axes of one
-element, against float64."""
+"""fa_qk_norm_rope and its gradient without an epsilon, with axes of one element,
+and where a warp takes many steps, against float64."""
 from __future__ import annotations
 
 import pytest
@@ -100,4 +100,69 @@ def test_strides_of_one_element_axes(D, shape, H, H_kv, axes):
     dyq, dyk = _odd(q.clone(), axes), _odd(k.clone(), axes)
     got = fa.qk_norm_rope_bwd(q, k, wq, wk, cs, pos, dyq, dyk, eps=EPS,
                               dq=_odd(torch.empty_like(q.contiguous()), axes))
+    _backward_ok(q, k, wq, wk, cs, pos, dyq, dyk, got, False, EPS)
+
+
+# ------------------------------------------------------------ many steps a warp
+# On 148 SMs, with a cache, the query rows of a token are chunks of 8, 6, 2, 4 and
+# 5 steps, the last one some rows short (without a cache two of them are cut), and
+# a warp walks 10 to 40 steps, so that every place of its ring is used again.
+@pytest.mark.parametrize("T,H,H_kv,D,rot,dtype,inter", [
+    (6000, 30, 6, 128, 128, BF16, False),
+    (9000, 44, 12, 64, 32, F16, True),
+    (1500, 47, 7, 128, 64, F16, True),      # chunks of 2 steps: a token's rows over several warps
+    (9000, 50, 18, 32, 32, BF16, False),
+    (5000, 130, 70, 16, 16, F16, False),
+])
+@pytest.mark.parametrize("cached", [False, True])
+def test_long_walks(T, H, H_kv, D, rot, dtype, inter, cached):
+    q, k, v, wq, wk, cs, pos = _inputs((T,), H, H_kv, D, rot, dtype, seed=T + D)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    pos = pos.long()
+    pos[torch.randperm(T, generator=g, device="cuda")[: T // 9]] = -1        # padding in between
+    pos[T // 2: T // 2 + 300] = -1
+    pos[7], pos[T - 1] = cs.shape[0], 1 << 40
+    real = (pos >= 0) & (pos < cs.shape[0])
+    qo, ko = torch.full_like(q, 5.0), torch.full_like(k, 5.0)
+    kw = {}
+    if cached:
+        page = 16
+        slots = torch.randperm(T + 200, generator=g, device="cuda")[:T]
+        slots[::13] = -1
+        caches = [torch.full((T // page + 14, page, H_kv, D), 7.0, dtype=dtype, device="cuda")
+                  for _ in range(2)]
+        kw = dict(v=v, k_cache=caches[0], v_cache=caches[1], slots=slots)
+    fa.qk_norm_rope(q, k, wq, wk, cs, pos, eps=EPS, interleaved=inter, q_out=qo, k_out=ko, **kw)
+    _rows_ok(qo[real], q[real], wq, cs, pos[real], inter)
+    _rows_ok(ko[real], k[real], wk, cs, pos[real], inter)
+    assert (qo[~real] == 5).all() and (ko[~real] == 5).all()
+    if cached:
+        kept = real & (slots >= 0)
+        for cache, rows in zip(caches, (ko, v)):
+            want = torch.full_like(cache, 7.0)
+            want.flatten(0, 1)[slots[kept]] = rows[kept]
+            assert torch.equal(cache, want)
+
+
+@pytest.mark.parametrize("wide", [False, True])
+def test_long_walks_to_heads_first(wide):
+    B, L, H, H_kv, D = 3, 2500, 22, 6, 64
+    q, k, _, wq, wk, cs, pos = _inputs((B, L), H, H_kv, D, D, BF16, seed=77)
+    pos = pos.long() if wide else pos
+    pos[1, 100:200], pos[2, -1] = -1, -3
+    qo = torch.full((B, H, L, D), 5.0, dtype=BF16, device="cuda")
+    ko = torch.full((B, H_kv, L, D), 5.0, dtype=BF16, device="cuda")
+    fa.qk_norm_rope(q, k, wq, wk, cs, pos, eps=EPS, q_out=qo.transpose(1, 2), k_out=ko.transpose(1, 2))
+    real = pos >= 0
+    for out, x, w in ((qo.transpose(1, 2), q, wq), (ko.transpose(1, 2), k, wk)):
+        _rows_ok(out[real], x[real], w, cs, pos[real], False)
+        assert (out[~real] == 5).all()
+
+
+@pytest.mark.parametrize("T,H,H_kv,D", [(6000, 30, 6, 128), (9000, 20, 12, 64)])
+def test_long_backward(T, H, H_kv, D):
+    q, k, _, wq, wk, cs, pos = _inputs((T,), H, H_kv, D, D, BF16, seed=T)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    dyq, dyk = (torch.randn(x.shape, generator=g, device="cuda").bfloat16() for x in (q, k))
+    got = fa.qk_norm_rope_bwd(q, k, wq, wk, cs, pos, dyq, dyk, eps=EPS)
     _backward_ok(q, k, wq, wk, cs, pos, dyq, dyk, got, False, EPS)
