@@ -1347,21 +1347,25 @@ extern "C" int fa_selftest_wait_timeout(int *result, cudaStream_t stream) {
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
+namespace fa {
+int paged_take_status();   // fa_paged_api.cu: its own status word
+#ifdef FA_TEST_HOOKS
+bool paged_set_withhold(int block);
+#endif
+}
+
 #ifdef FA_TEST_HOOKS
 // Watchdog test library only (include/fa_test_hooks.h): the key block whose
-// copy the K producer of CTA 0 withholds in the forward kernel (-1: none).
+// copy the K producer of CTA 0 withholds in the forward kernels (-1: none).
 extern "C" int fa_test_set_withhold(int block) {
-  if (cudaMemcpyToSymbol(fa::g_fa_test_withhold_block, &block, sizeof(int)) != cudaSuccess) {
+  if (cudaMemcpyToSymbol(fa::g_fa_test_withhold_block, &block, sizeof(int)) != cudaSuccess ||
+      !fa::paged_set_withhold(block)) {
     cudaGetLastError();
     return FA_ERR_CUDA;
   }
   return FA_OK;
 }
 #endif
-
-namespace fa {
-int paged_take_status();   // fa_paged_api.cu: its own status word
-}
 
 extern "C" int fa_get_device_status(cudaStream_t stream) {
   if (cudaStreamSynchronize(stream) != cudaSuccess) return FA_ERR_CUDA;
@@ -1372,11 +1376,9 @@ extern "C" int fa_get_device_status(cudaStream_t stream) {
     if (cudaMemcpyToSymbol(g_fa_status, &zero, sizeof(zero)) != cudaSuccess)
       return FA_ERR_CUDA;
   }
-#ifndef FA_TEST_HOOKS   // the watchdog test library is built without that unit
   const int paged = paged_take_status();
   if (paged < 0) return FA_ERR_CUDA;
   st |= static_cast<unsigned int>(paged);
-#endif
   return st != 0 ? FA_ERR_TIMEOUT : FA_OK;
 }
 

@@ -86,8 +86,9 @@ constexpr int kBalMaxEntries = 74;         // cluster pairs per item: at most 14
 #ifdef FA_TEST_HOOKS
 // Watchdog test library only (never in libfa.so): the K producer of CTA 0
 // skips the copy of this key block (-1: none), so that the MMA warp's
-// bounded wait for it runs out and the abort path of every role runs.
-__device__ int g_fa_test_withhold_block = -1;
+// bounded wait for it runs out and the abort path of every role runs.  (Each
+// translation unit has its own, as of the status word.)
+static __device__ int g_fa_test_withhold_block = -1;
 #endif
 
 struct FwdParams {

@@ -29,6 +29,12 @@ int paged_take_status() {
   return st != 0 ? 1 : 0;
 }
 
+#ifdef FA_TEST_HOOKS
+bool paged_set_withhold(int block) {
+  return cudaMemcpyToSymbol(g_fa_test_withhold_block, &block, sizeof(int)) == cudaSuccess;
+}
+#endif
+
 namespace {
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
@@ -219,6 +225,10 @@ extern "C" int fa_fwd_paged(const void *q, long long q_stride_t, long long q_str
       !encode(&p.tm_v, v_cache, dtype, 4, cd, cs, cb))
     return FA_ERR_CUDA;
   switch (D * 2 + dtype) {
+#ifdef FA_TEST_HOOKS   // the watchdog test library: fp16 head dims 64 and 128 only
+    case 128: return launch_paged<64, 0>(p, grid, stream);
+    case 256: return launch_paged<128, 0>(p, grid, stream);
+#else
     case 32: return launch_paged<16, 0>(p, grid, stream);
     case 33: return launch_paged<16, 1>(p, grid, stream);
     case 64: return launch_paged<32, 0>(p, grid, stream);
@@ -235,6 +245,7 @@ extern "C" int fa_fwd_paged(const void *q, long long q_stride_t, long long q_str
     case 225: return launch_paged<112, 1>(p, grid, stream);
     case 256: return launch_paged<128, 0>(p, grid, stream);
     case 257: return launch_paged<128, 1>(p, grid, stream);
+#endif
   }
   return FA_ERR_HEADDIM;
 }

@@ -63,6 +63,7 @@ constexpr int kSchedWarp = 11;       // walks the work, loads Q
 constexpr int kPagedMinUnits = 3;    // cost a CTA gets at least (4: single tokens 2 us slower)
 constexpr int kPagedRows = 2 * kBM;  // rows of a work item
 constexpr int kItemRing = 3;         // items announced ahead
+constexpr uint32_t kCountedBar = 1;  // named barrier: warp 0 has left its role
 // A single tile of at most this many rows (decoding) takes TMEM in the layout of a
 // matrix fragment: four lanes share a row, 32 of a block's 128 exponentials each.
 // One warp's 128 of a lane had set the pace (128 requests over 500 tokens, H32/8
@@ -71,6 +72,10 @@ constexpr int kItemRing = 3;         // items announced ahead
 // to 16 bits took off, so the same products sum it, and the epilogue adds row
 // g + 8 to row g: weights of 16 bits (bf16) or 22 (fp16) of precision.
 constexpr int kFewRows = 8;
+
+#ifdef FA_TEST_HOOKS
+constexpr int kWithholdV = 1 << 16;   // g_fa_test_withhold_block: this + n is V's n-th fill
+#endif
 
 struct PagedParams {
   CUtensorMap tm_q;   // (D, H, total_q), box (cols, G, TQ)
@@ -236,7 +241,7 @@ struct PagedCuts {
 };
 
 // All threads: the line's length and the requests that the ends of this CTA's
-// piece lie in.  Ends with a barrier.
+// piece lie in.  The caller's barrier makes them visible.
 __device__ __forceinline__ void paged_find_piece(const PagedParams &p, PagedSetup &st,
                                                  PagedCuts &cuts) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -928,9 +933,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       t = ahead;
     }
-    if (!ok)   // let the copies in flight land before the CTA exits
+    if (!ok || *abort_flag)   // let the copies in flight land before the CTA exits
       for (int n = max(0, nq - 2); n < nq; ++n)
         mbar_wait_slow(smem_u32(&bars->q_full[n & 1]), (n >> 1) & 1, abort_flag, false);
+    named_barrier_sync(kCountedBar, 64);   // thread 0 counts no more parts
+    if (*abort_flag) {
+      // the others are counted here, so that the tickets end at 0 for a captured
+      // call's next run (in this role: its registers are what the walk needs)
+      walk.start(p, bars->setup, cuts);
+      while (walk.next(p, t))
+        if (t.slot >= 0 && lane == 0 && !bars->ticketed[t.slot]) paged_ticket(p, walk.cut_of(cuts));
+    }
   } else if (warp == kLoadWarp || warp == kLoadWarpV) {
     // =================================================== K and V producers
     // Lane i copies the i-th run of box_rows rows of a key block (one page, or
@@ -944,6 +957,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int per_block = kBN / p.box_rows;          // copies of rows per block
     const int in_mask = (1 << p.page_shift) - 1;
     const uint64_t pol_keep = policy_evict_last(), pol_stream = policy_evict_first();
+#ifdef FA_TEST_HOOKS
+    const int withheld = blockIdx.x != 0 || g_fa_test_withhold_block < 0 ? -1
+                         : is_k ? g_fa_test_withhold_block
+                                : g_fa_test_withhold_block - kWithholdV;
+#else
+    constexpr int withheld = -1;
+#endif
     PagedItem t;
     int q = 0;             // fills so far
     int ragged = 0;        // V: ragged blocks so far
@@ -1022,9 +1042,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
         }
         const uint32_t bar = smem_u32(rag ? &bars->v_ragged : &bars->full[slot]);
-        if (lane == 0) mbar_arrive_expect_tx(bar, G::kTileBytes);
+        const bool given = withheld < 0 || q != withheld;   // (always, but in the watchdog test library)
+        if (lane == 0 && given) mbar_arrive_expect_tx(bar, G::kTileBytes);
         __syncwarp();
-        if (lane < per_block) {
+        if (lane < per_block && given) {
           const int in_page = (k0 + lane * p.box_rows) & in_mask;
           if (page < 0 || page >= p.n_pages) page = p.n_pages;
           const uint32_t dst = sRing + slot * G::kTileBytes + lane * p.box_rows * G::kSwBytes;
@@ -1044,7 +1065,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (ok && pend_slot >= 0) finish_ragged();
-    if (!ok) {
+    if (!ok || *abort_flag) {
       // let the copies in flight land before the CTA exits; a ragged block's
       // copy lands on v_ragged
       if (pend_slot >= 0)
@@ -1646,18 +1667,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         // for the next part)
       }
     }
+    if (warp == 0) named_barrier_arrive(kCountedBar, 64);
   }
 
   // ---- teardown
   tc_fence_before_sync();
   __syncthreads();
-  if (*abort_flag && warp == kSchedWarp) {
-    // every part is counted, so that the tickets end at 0 for the next call
-    PagedItem t;
-    walk.start(p, bars->setup, cuts);
-    while (walk.next(p, t))
-      if (t.slot >= 0 && lane == 0 && !bars->ticketed[t.slot]) paged_ticket(p, walk.cut_of(cuts));
-  }
   if (warp == kMmaWarp) {
     tc_fence_after_sync();
     mbar_wait_slow(smem_u32(&bars->mma_done), 0, abort_flag, false);
