@@ -712,7 +712,8 @@ def paged_plan(q_lens, ctx_lens, block_table, free_pages, page_size, num_tokens,
     captured graph's padding, gets -1).  ``out``: a PagedPlan to write into;
     otherwise its tensors share one allocation.  They may not overlap the
     inputs: ctx_lens cannot be out.kv_lens.  Nothing is read back: counts[2] > 0
-    tells that pages ran out."""
+    tells that pages ran out, in this step or in an earlier one for tokens that
+    continue its page."""
     r = (_ext or _serving()).paged_plan(q_lens, ctx_lens, block_table, free_pages, page_size,
                                         num_tokens, out, _handle(stream))
     return PagedPlan._make(r) if out is None else out
@@ -729,7 +730,9 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps=1e-6, interle
     q_weight, k_weight: [D] of q's dtype, or None (no norm).  cos_sin: float32
     [max_pos, rot_dim], the cosines then the sines.  positions: int32 or int64
     of q's token axes; a negative one (or >= max_pos) marks padding, of which
-    nothing is written.  ``interleaved``: pairs (2i, 2i + 1) instead of
+    nothing is written: its rows of an output allocated here hold what the
+    memory held, and a position that cos_sin has no row for is lost without a
+    word.  ``interleaved``: pairs (2i, 2i + 1) instead of
     (i, i + rot_dim / 2).
 
     q_out, k_out: like q, k, any strides (a [B, H, L, D] tensor transposed),
@@ -764,7 +767,9 @@ def flash_fwd_paged(q, k_cache, v_cache, block_table, cu_q, kv_lens, scale=None,
     cu_q[b + 1] (int32 [B + 1]); k_cache, v_cache: [pages, page_size, H_kv, D],
     any strides, page_size a power of two, at least 16; block_table: int32
     [B, max_pages]; kv_lens: int32 [B], tokens in the cache with the new ones.
-    Causal and window positions count to the end of the request.  ``scale``
+    Causal and window positions count to the end of the request.  Up to 8 new
+    tokens times H / H_kv a request (decoding) keep their softmax weights to 16
+    bits or more, larger tiles round them to q's dtype as flash_fwd does.  ``scale``
     defaults to 1/sqrt(D).  The workspace is allocated here unless given (a
     uint8 CUDA tensor of fa_paged_workspace_bytes(D), 256-byte aligned).
     Returns (out [total_q, H, D], lse float32 [total_q, H] or None); rows no

@@ -35,12 +35,15 @@
 // the next S_t is computed while the softmax works on this one.
 //
 // Measured, back to back (of the copy rate, of the bf16 burst): decoding 64
-// requests over 4k to 12k tokens, H32/8 D128, 336 us (2.0 GB, 0.92); two chunks
-// of up to 4096 tokens over up to 12k, H32/8 D128, 1360 us (0.60; the board's
-// power limit, 1170 us and 0.70 alone); 14 decoding requests beside 6 chunks of
-// 250 to 475 tokens, window 4096, H16 D64, 134 us (0.36; the exponentials of the
-// chunks and the latency of an item's ends); one request over 800 tokens, H32/8
-// D128, 16 us (launch, set-up 3, one block's chain 4, joining 5).
+// requests over 4k to 12k tokens, H32/8 D128, 319 us (2.0 GB, 0.97; 352 us on the
+// slowest card); two chunks of up to 4096 tokens over up to 12k, H32/8 D128,
+// 1350 us (0.61; the board's power limit, with pauses between the calls 1205 us
+// and 0.68); 14 decoding requests beside 6 chunks of 250 to 475 tokens, window
+// 4096, H16 D64, 133 us (0.37; the exponentials of the chunks and the latency of
+// an item's ends); one request over 800 tokens, H32/8 D128, 16.6 us (launch,
+// set-up 3, one block's chain 4, joining 5); 64 requests over 1000 tokens with 1,
+// 2 and 4 new ones (4, 8 and 16 rows a tile), H32/8 D128, 57, 60 and 68 us (bytes
+// 40): from 9 rows on a lane does all 128 exponentials of its row.
 //
 // The weights P enter the product with V in 16 bits, as the tensor cores take
 // them beside a 16-bit V and as in the dense forward; the normaliser sums them

@@ -14,21 +14,21 @@
 // of one token) belongs to D / 16 lanes, each with two 16-byte vectors that
 // hold whole pairs (8 values from each half, or 16 neighbours), so the rotation
 // needs no exchange and only the norm's sum crosses lanes.  Rows are copied to
-// shared memory some steps ahead.  All arithmetic is fp32; the result is
-// rounded once.  Measured: forward 0.85 of the HBM copy rate at B4 L8192 H48
-// D64 (145 us), 0.78 with the cache at 8192 tokens (40 us); gradient 0.81 at B2
-// L16384 H32/8 D128 (191 us); cards differ by some 5 %.
+// shared memory two steps ahead.  All arithmetic is fp32; the result is
+// rounded once.  Measured: forward 0.87 of the HBM copy rate at B4 L8192 H48
+// D64 (142 us), 0.78 with the cache at 8192 tokens (40 us); gradient 0.84 at B2
+// L16384 H32/8 D128 (183 us); up to 4 % more on other cards.
 #pragma once
 
 #include "sm100.cuh"
 
 namespace fa {
 
-// Stages and blocks per SM, measured on 8192 tokens (32 + 8 + 8 rows of D 128,
-// to the cache) and on B4 L8192 H48 D64: 3 stages, 4 blocks 45 / 141 us; 2
-// stages 54 / 178, 4 stages 45 / 150 (more shared memory, less L1); 3 blocks
-// 49 / 158, 5 blocks 47 / 152.  The gradient at B2 L16384 H32/8 D128: 3 stages,
-// 4 blocks 183 us; 2 stages 212; 4 stages 189.
+// Stages and blocks per SM, measured on one card on 8192 tokens (32 + 8 + 8 rows
+// of D 128, to the cache) and on B4 L8192 H48 D64: 3 stages, 4 blocks 40 / 142 us;
+// 2 stages 50 / 175; 4 stages 39 / 139, for a third more shared memory; 3 blocks
+// 45 / 156, 5 blocks 41 / 148.  The gradient at B2 L16384 H32/8 D128: 3 stages,
+// 4 blocks 183 us; 2 stages 206; 4 stages 182.
 constexpr int kRopeThreads = 128;
 constexpr int kRopeStages = 3;        // rows a lane has in shared memory
 constexpr int kRopeBlocks = 4;        // resident per SM

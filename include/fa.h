@@ -367,6 +367,8 @@ int fa_fwd_splitkv_static(const void *q, const void *k, const void *v, void *out
  * [page, head, token, D] both fit.  Slot s is row s % page_size of page
  * s / page_size.  Token x of request b lies in slot
  * block_table[b * table_stride + x / page_size] * page_size + x % page_size.
+ * fa_paged_plan and fa_qk_norm_rope take any page_size >= 1, fa_fwd_paged powers
+ * of two from 16 on.
  */
 
 /*
@@ -440,7 +442,7 @@ typedef struct {
  * same slot.
  *
  * A token whose position is negative or >= max_pos is padding: nothing of it
- * is written.  A token whose slot is negative or >= num_pages * page_size
+ * is written, so cos_sin has to have a row for every position in use.  A token whose slot is negative or >= num_pages * page_size
  * writes no cache.  L == 0 is a no-op.
  * Errors: FA_ERR_ARG for a bad rot_dim, eps, page_size or num_pages;
  * FA_ERR_ALIGN for a misaligned pointer or stride; others as fa_fwd.
