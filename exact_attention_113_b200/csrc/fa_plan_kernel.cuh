@@ -87,6 +87,19 @@ __global__ void __launch_bounds__(kPlanThreads) fa_plan_kernel(const PlanParams 
       ip += grown[e];
     }
     const long long mine_t = it, mine_p = ip;
+    // New tokens that continue a partly filled page have no slot where an earlier
+    // step got none.  (Its entry is old: no block writes it; it arrives meanwhile.)
+    int filled[kEach], entry[kEach];
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      filled[e] = entry[e] = 0;
+      const int have = pages_of(ctx[e]);
+      const unsigned left = static_cast<unsigned>(have) * P - static_cast<unsigned>(ctx[e]);
+      if (counts && left != 0 && have <= p.max_pages) {
+        filled[e] = min(q[e], static_cast<int>(left));
+        entry[e] = p.table[(base + tid * kEach + e) * p.table_stride + have - 1];
+      }
+    }
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const long long a = __shfl_up_sync(0xffffffffu, it, d), c = __shfl_up_sync(0xffffffffu, ip, d);
@@ -130,13 +143,7 @@ __global__ void __launch_bounds__(kPlanThreads) fa_plan_kernel(const PlanParams 
         const long long room =
             (static_cast<long long>(min(pages_of(ctx[e]), p.max_pages)) + got) * P - ctx[e];
         missing += q[e] - min(static_cast<long long>(q[e]), max(room, 0ll));
-        // and those in the partly filled page that they continue, where an earlier
-        // step got none (its entry is old: no block writes it)
-        const unsigned c = static_cast<unsigned>(ctx[e]), size = static_cast<unsigned>(P);
-        const unsigned in_page = c % size, at_page = c / size;
-        if (in_page != 0 && q[e] > 0 && at_page < static_cast<unsigned>(p.max_pages) &&
-            p.table[(base + i) * p.table_stride + at_page] < 0)
-          missing += min(q[e], P - static_cast<int>(in_page));
+        if (entry[e] < 0) missing += filled[e];
       }
       at += q[e];
       first += grown[e];
