@@ -112,18 +112,18 @@ struct PagedReq {
 };
 
 // Lengths of request b, cut to the tensors: no access lies outside them, and
-// the tokens that have a row keep their positions.  (kv_lens and cu_q may hold
-// anything; a position is at most 2^30 from 0 with all tokens of the request, so
-// that sums with a window stay ints.)
+// the tokens that have a row keep their positions.  cu_q and kv_lens may hold
+// anything: with a row (q_start < e) `first` is above -2^31 before its bound and
+// the last position below 2^30, so these and their sums with a window are ints;
+// without one it is not used.
 __device__ __forceinline__ PagedReq paged_req(const PagedParams &p, int b) {
   PagedReq r;
   const int a = __ldg(p.cu_q + b), e = __ldg(p.cu_q + b + 1);
   r.q_start = min(max(a, 0), p.total_q);
   r.q_len = max(min(e, p.total_q) - r.q_start, 0);
-  const int kv = max(__ldg(p.kv_lens + b), 0);
+  const int kv = min(max(__ldg(p.kv_lens + b), 0), 1 << 30);
   r.kv_len = min(kv, p.max_kv);
-  const long long first = static_cast<long long>(kv) - e + r.q_start;
-  r.first = static_cast<int>(max(min(first, (1ll << 30) - r.q_len), -(1ll << 30)));
+  r.first = r.q_len > 0 ? max(kv - (e - r.q_start), -(1 << 30)) : 0;
   return r;
 }
 
@@ -391,7 +391,7 @@ struct PagedWalk {
     h = 0;
     if (++b >= p.B) return;
     r = paged_req(p, b);
-    if (r.q_len > 0) return;
+    if (__builtin_expect(r.q_len > 0, 1)) return;
     constexpr int kLook = 4;
     const int lane = threadIdx.x & 31;
     for (++b; b < p.B; b += 32 * kLook) {
@@ -940,7 +940,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int n = max(0, nq - 2); n < nq; ++n)
         mbar_wait_slow(smem_u32(&bars->q_full[n & 1]), (n >> 1) & 1, abort_flag, false);
     named_barrier_sync(kCountedBar, 64);   // thread 0 counts no more parts
-    if (*abort_flag) {
+    if (__builtin_expect(*abort_flag != 0, 0)) {
       // the others are counted here, so that the tickets end at 0 for a captured
       // call's next run (in this role: its registers are what the walk needs)
       walk.start(p, bars->setup, cuts);
