@@ -630,10 +630,10 @@ __device__ __forceinline__ void paged_store16(const PagedParams &p, uint8_t *oro
 
 // The results of up to kFewRows rows: a lane takes row g = lane / 4 of TMEM and
 // row g + 8, the same columns of what the weights' rounding took off, so that
-// their sum needs no exchange (64 requests over 1000, H32/8 D128: 59.2 us with rows
-// in lanes and shuffles, so 56.0; before there were rests to add, 56.4).  As in the
-// general epilogue a warpgroup joins every other 16 columns of the two O; sa, sb:
-// their factors, of row `lane`.
+// their sum needs no exchange (64 requests over 1000, H32/8 D128: 59 us with rows
+// in lanes and shuffles, so 57, as without rests to add).  As in the general
+// epilogue a warpgroup joins every other 16 columns of the two O; sa, sb: their
+// factors, of row `lane`.
 template <int D, int DT>
 __device__ __forceinline__ void paged_few_rows(const PagedParams &p, const PagedItem &t,
                                                uint32_t from, int u, int tok_of_g, bool none,
@@ -645,6 +645,8 @@ __device__ __forceinline__ void paged_few_rows(const PagedParams &p, const Paged
 #pragma unroll
   for (int i = 0; i < kChunks; ++i) o[i][0] = o[i][1] = make_float2(0.0f, 0.0f);
   auto held = [&](int i) { return 32 * i + 16 < D || u == 0; };
+  // (beside an infinite value the rests, which may be 0 or of the other sign, are none)
+  auto with_rest = [](float x, float rest) { return fabsf(x) < INFINITY ? x + rest : x; };
   auto add = [&](uint32_t at, float w) {
     uint32_t x[kChunks][8];
 #pragma unroll
@@ -657,8 +659,8 @@ __device__ __forceinline__ void paged_few_rows(const PagedParams &p, const Paged
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const uint32_t *v = x[i] + 4 * e;
-        o[i][e].x += w * (__uint_as_float(v[0]) + __uint_as_float(v[2]));
-        o[i][e].y += w * (__uint_as_float(v[1]) + __uint_as_float(v[3]));
+        o[i][e].x += w * with_rest(__uint_as_float(v[0]), __uint_as_float(v[2]));
+        o[i][e].y += w * with_rest(__uint_as_float(v[1]), __uint_as_float(v[3]));
       }
     }
   };

@@ -13,10 +13,10 @@
 // its own 1024 tokens and its share of the new pages, so no block waits for
 // another (5 to 6 us for 8 requests, as long as the host's call; 8.2 us for 1024
 // requests of 197k tokens, of which the bytes are 0.4: the scan, then the new
-// pages and four tokens a thread, one search, load and store after the other).  A token or page finds
-// its request by a search in the tile's prefix sums.  A new token's page is
-// taken from the free list directly, not from the table that another block may
-// be writing.
+// pages and four tokens a thread, one search, load and store after the other).
+// A token or page finds its request by a search in the tile's prefix sums.  A new
+// token's page is taken from the free list directly, not from the table that
+// another block may be writing.
 #pragma once
 
 #include <cuda_runtime.h>

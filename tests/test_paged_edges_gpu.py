@@ -56,6 +56,26 @@ def test_weights_of_one_request_cut_over_all_ctas():
     assert ((out.double() - want).abs() <= _exact_weights_bound(want, mag, total, BF16))[:1].all()
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("D", [64, 128])
+def test_infinite_values_of_visible_keys(D, dtype):
+    # equal scores: every weight is 1, and exact, so its rest is 0
+    b = Batch([1, 2, 1], [7, 300, 40], 8, 2, D, dtype, 16, seed=33)
+    b.q.zero_()
+    want, _ = b.run()
+    spots = ((0, 3, 1, math.inf), (1, 150, 0, -math.inf), (2, 39, 0, math.inf))
+    for r, key, head, x in spots:
+        page, row = int(b.table[r, key // 16]), key % 16
+        b.v[page, row, head, 5] = x
+    out, lse = b.run()
+    assert torch.isfinite(lse[: int(b.cu_q[-1])]).all()
+    for r, key, head, x in spots:
+        rows, heads = slice(int(b.cu_q[r]), int(b.cu_q[r + 1])), slice(4 * head, 4 * head + 4)
+        assert (out[rows, heads, 5] == x).all()
+        want[rows, heads, 5] = x
+    assert torch.equal(out, want)
+
+
 # ------------------------------------------------------------ cut requests
 def _close(out, lse, want, dtype):
     o, e, mag, total = want
